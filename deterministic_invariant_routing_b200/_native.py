@@ -40,6 +40,15 @@ MOE_STAGE_STATS = 5
 MOE_STAGE_BACKWARD = 6
 MOE_NUM_STAGE_EVENTS = 8
 
+MOE_BF16 = 0
+MOE_F16 = 1
+MOE_F32 = 2
+
+MOE_GATE_NONE = 0
+MOE_GATE_CHANNEL = 1
+MOE_GATE_TOKEN = 2
+MOE_GATE_FULL = 3
+
 
 class MoeCfg(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("E", ctypes.c_int32),
@@ -49,10 +58,20 @@ class MoeCfg(ctypes.Structure):
                 ("topk_group", ctypes.c_int32)]
 
 
+class MoeNormCfg(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("first_row", ctypes.c_int64), ("p", ctypes.c_double),
+                ("H", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("param_dtype", ctypes.c_int32), ("gate", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float),
+                ("branch_scale", ctypes.c_float)]
+
+
 _P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _CFG = ctypes.POINTER(MoeCfg)
 _I = ctypes.c_int
+_NCFG = ctypes.POINTER(MoeNormCfg)
+_I64 = ctypes.c_int64
 
 SIGNATURES = {
     "moe_workspace_bytes": (_SZ, [_CFG, _I]),
@@ -69,6 +88,11 @@ SIGNATURES = {
     "moe_forward_train": (_I, [_CFG] + [_P] * 15 + [_SZ, _P]),
     "moe_forward_host_workspace_bytes": (_SZ, [_CFG, _I]),
     "moe_forward_host": (_I, [_CFG, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _SZ, _P]),
+    "moe_residual_norm": (_I, [_NCFG] + [_P] * 10),
+    "moe_residual_norm_workspace_bytes": (_SZ, [_NCFG]),
+    "moe_residual_norm_backward": (_I, [_NCFG] + [_P] * 15 + [_SZ, _P]),
+    "moe_dropout": (_I, [_I64, ctypes.c_int32, ctypes.c_int32, ctypes.c_double, _P, _P, _I64, _P,
+                         _P, _P]),
     "moe_status_string": (ctypes.c_char_p, [_I]),
     "moe_abi_version": (_I, []),
     "moe_pipeline_wait_selftest": (_I, [_P, ctypes.c_longlong, _P]),

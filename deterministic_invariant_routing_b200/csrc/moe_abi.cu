@@ -4,6 +4,7 @@
 #include <math.h>
 #include <string.h>
 
+#include <initializer_list>
 #include <mutex>
 
 #include "moe_internal.cuh"
@@ -82,6 +83,29 @@ int check_cfg(const moe_cfg* c)
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int check_norm_cfg(const moe_norm_cfg* c)
+{
+    if (c == nullptr) return MOE_ERR_ARG;
+    if (c->T < 0 || c->T >= ((int64_t)1 << 31)) return MOE_ERR_SHAPE;
+    if (c->H < 8 || c->H > 16384 || c->H % 8 != 0) return MOE_ERR_SHAPE;
+    if (c->first_row < 0 || c->first_row > ((int64_t)1 << 32) - c->T) return MOE_ERR_SHAPE;
+    if (c->dtype != MOE_BF16 && c->dtype != MOE_F16 && c->dtype != MOE_F32) return MOE_ERR_SHAPE;
+    if (c->param_dtype != MOE_F32 && c->param_dtype != c->dtype) return MOE_ERR_SHAPE;
+    if (c->gate < MOE_GATE_NONE || c->gate > MOE_GATE_FULL) return MOE_ERR_SHAPE;
+    if (!(c->p >= 0.0 && c->p <= 1.0)) return MOE_ERR_SHAPE;
+    if (!(c->eps > 0.0f) || !isfinite(c->eps)) return MOE_ERR_SHAPE;
+    if (!isfinite(c->residual_scale) || !isfinite(c->branch_scale)) return MOE_ERR_SHAPE;
+    return MOE_OK;
+}
+
+// every pointer of the list is NULL or 16-byte aligned
+int check_aligned(std::initializer_list<const void*> ps)
+{
+    for (const void* p : ps)
+        if (!aligned16(p)) return MOE_ERR_ARG;
+    return MOE_OK;
+}
 
 int check_device()
 {
@@ -1127,6 +1151,94 @@ MOE_API int moe_forward_train(const moe_cfg* cfg, const uint16_t* x, const uint1
     }
     return cuda_rc(launch_combine(c, at<uint16_t>(ws, L.y), topk_w, at<int32_t>(ws, L.dest_pad),
                                   y_s, token_mask, out, st));
+}
+
+MOE_API int moe_residual_norm(const moe_norm_cfg* cfg, const void* x, const void* y,
+                              const void* w_post, const void* gate, const void* w_next,
+                              const int64_t* rng, const int32_t* row_ids, void* r, void* n,
+                              void* stream)
+{
+    int rc = check_norm_cfg(cfg);
+    if (rc != MOE_OK || cfg->T == 0) return rc;  // no rows: the per-token pointers may be NULL
+    if ((w_next == nullptr) != (n == nullptr)) return MOE_ERR_ARG;
+    if ((cfg->gate == MOE_GATE_NONE) != (gate == nullptr)) return MOE_ERR_ARG;
+    if (y == nullptr) {
+        if (w_post != nullptr || gate != nullptr || r != nullptr || w_next == nullptr ||
+            cfg->residual_scale != 1.0f || cfg->p != 0.0)
+            return MOE_ERR_ARG;
+    } else if (r == nullptr) {
+        return MOE_ERR_ARG;
+    }
+    if (x == nullptr || (cfg->p > 0.0 && rng == nullptr)) return MOE_ERR_ARG;
+    if ((rc = check_aligned({x, y, w_post, w_next, r, n})) != MOE_OK) return rc;
+    if (cfg->gate != MOE_GATE_TOKEN && !aligned16(gate)) return MOE_ERR_ARG;
+    if ((rc = check_device()) != MOE_OK) return rc;
+    return cuda_rc(launch_residual_norm(*cfg, x, y, w_post, gate, w_next, rng, row_ids, r, n,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+MOE_API size_t moe_residual_norm_workspace_bytes(const moe_norm_cfg* cfg)
+{
+    return check_norm_cfg(cfg) == MOE_OK ? residual_norm_bwd_ws_bytes(*cfg) : 0;
+}
+
+MOE_API int moe_residual_norm_backward(const moe_norm_cfg* cfg, const void* r, const void* y,
+                                       const void* w_post, const void* gate, const void* w_next,
+                                       const int64_t* rng, const int32_t* row_ids,
+                                       const void* dr, const void* dn, void* dx, void* dy,
+                                       float* dw_post, void* dgate, float* dw_next, void* ws,
+                                       size_t ws_bytes, void* stream)
+{
+    int rc = check_norm_cfg(cfg);
+    if (rc != MOE_OK) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (cfg->T == 0) {  // the per-token pointers may be NULL; parameter gradients are zero
+        if ((rc = check_device()) != MOE_OK) return rc;
+        const size_t bytes = (size_t)cfg->H * sizeof(float);
+        float* sums[] = {dw_post, dw_next,
+                         cfg->gate == MOE_GATE_CHANNEL ? static_cast<float*>(dgate) : nullptr};
+        for (float* p : sums)
+            if (p != nullptr && (rc = cuda_rc(cudaMemsetAsync(p, 0, bytes, st))) != MOE_OK)
+                return rc;
+        return MOE_OK;
+    }
+    if ((w_next == nullptr) != (dn == nullptr) || (w_next == nullptr) != (dw_next == nullptr) ||
+        (w_post == nullptr) != (dw_post == nullptr) || (gate == nullptr) != (dgate == nullptr) ||
+        (cfg->gate == MOE_GATE_NONE) != (gate == nullptr) || (y == nullptr) != (dy == nullptr))
+        return MOE_ERR_ARG;
+    if (y == nullptr && (w_post != nullptr || gate != nullptr || w_next == nullptr ||
+                         cfg->residual_scale != 1.0f || cfg->p != 0.0))
+        return MOE_ERR_ARG;
+    if (dx == nullptr || (dr == nullptr && dn == nullptr) || (w_next != nullptr && r == nullptr) ||
+        (cfg->p > 0.0 && rng == nullptr))
+        return MOE_ERR_ARG;
+    if ((rc = check_aligned({r, y, w_post, w_next, dr, dn, dx, dy})) != MOE_OK) return rc;
+    if (cfg->gate != MOE_GATE_TOKEN && (!aligned16(gate) || !aligned16(dgate))) return MOE_ERR_ARG;
+    const size_t need = residual_norm_bwd_ws_bytes(*cfg);
+    if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned16(ws))) return MOE_ERR_WORKSPACE;
+    if ((rc = check_device()) != MOE_OK) return rc;
+    return cuda_rc(launch_residual_norm_bwd(*cfg, r, y, w_post, gate, w_next, rng, row_ids, dr, dn,
+                                            dx, dy, dw_post, dgate, dw_next, ws, st));
+}
+
+MOE_API int moe_dropout(int64_t T, int32_t H, int32_t dtype, double p, const void* x,
+                        const int64_t* rng, int64_t first_row, const int32_t* row_ids, void* out,
+                        void* stream)
+{
+    moe_norm_cfg c{};
+    c.T = T;
+    c.first_row = first_row;
+    c.p = p;
+    c.H = H;
+    c.dtype = c.param_dtype = dtype;
+    c.eps = 1.0f;
+    int rc = check_norm_cfg(&c);
+    if (rc != MOE_OK || T == 0) return rc;
+    if (x == nullptr || out == nullptr || rng == nullptr) return MOE_ERR_ARG;
+    if ((rc = check_aligned({x, out})) != MOE_OK) return rc;
+    if ((rc = check_device()) != MOE_OK) return rc;
+    return cuda_rc(launch_dropout(T, H, dtype, p, x, rng, first_row, row_ids, out,
+                                  static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -111,6 +111,23 @@ cudaError_t launch_pad_rows(const int32_t* ids, const int32_t* dest_row, const i
 cudaError_t launch_zero_pad_rows(uint16_t* buf, int64_t cols, const int32_t* off,
                                  const int32_t* poff, int G, cudaStream_t st);
 
+// block seams (block.cu): norm, gate, dropout, residual and norm, with gradients
+uint32_t dropout_threshold(double p);
+float dropout_scale(uint32_t threshold);
+cudaError_t launch_residual_norm(const moe_norm_cfg& c, const void* x, const void* y,
+                                 const void* w_post, const void* gate, const void* w_next,
+                                 const int64_t* rng, const int32_t* row_ids, void* r, void* n,
+                                 cudaStream_t st);
+size_t residual_norm_bwd_ws_bytes(const moe_norm_cfg& c);
+cudaError_t launch_residual_norm_bwd(const moe_norm_cfg& c, const void* r, const void* y,
+                                     const void* w_post, const void* gate, const void* w_next,
+                                     const int64_t* rng, const int32_t* row_ids, const void* dr,
+                                     const void* dn, void* dx, void* dy, float* dw_post,
+                                     void* dgate, float* dw_next, void* ws, cudaStream_t st);
+cudaError_t launch_dropout(int64_t T, int32_t H, int dtype, double p, const void* x,
+                           const int64_t* rng, int64_t first_row, const int32_t* row_ids,
+                           void* out, cudaStream_t st);
+
 // tensor-core GEMMs (tcgen05 / TMEM / TMA)
 //   EPI_SWIGLU      out[r, c] = bf16(silu(g) * u) of A . B_g^T (gate and up columns paired)
 //   EPI_BF16        out[r, c] = bf16(A . B_g^T)

@@ -252,6 +252,162 @@ def router_stats(cfg: Config, logits, offsets, token_mask=None):
     return {"tokens_per_expert": counts, "mean_prob": mp, "aux": aux}
 
 
+# ------------------------------------------------------------------ around the layer
+
+_DTYPES = {torch.bfloat16: N.MOE_BF16, torch.float16: N.MOE_F16, torch.float32: N.MOE_F32}
+
+
+def _call(dev: torch.device, fn, *args):
+    """fn(*args, stream) on dev's current stream, with dev the current device."""
+    if dev.type != "cuda":
+        raise MoeError(f"tensors on {dev}, expected a CUDA device")
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        return fn(*args, _stream(dev))
+    with torch.cuda.device(dev):
+        return fn(*args, _stream(dev))
+
+
+def _act(t, name, shape=None, dtype=None, dev=None):
+    """A contiguous 2-D activation of a supported type."""
+    if t is None:
+        raise MoeError(f"{name} is required")
+    if t.dtype not in _DTYPES or t.dim() != 2:
+        raise MoeError(f"{name}: a 2-D bf16, fp16 or fp32 tensor is expected, got {t.dtype} "
+                       f"{tuple(t.shape)}")
+    return _need(t, name, t.dtype if dtype is None else dtype, t.shape if shape is None else shape,
+                 t.device if dev is None else dev)
+
+
+def rng_state(seed: int, offset: int = 0, device="cuda") -> torch.Tensor:
+    """The device state of the dropout masks, int64 (seed, offset): calls that share it share
+    their masks. Change it (in place, under a captured graph) to draw new ones."""
+    wrap = [(int(v) + 2 ** 63) % 2 ** 64 - 2 ** 63 for v in (seed, offset)]
+    return torch.tensor(wrap, dtype=torch.int64, device=device)
+
+
+def _norm_setup(x, y, w_post, gate, w_next, eps, residual_scale, branch_scale, p, rng, first_row,
+                row_ids):
+    """Checks shared by residual_norm and its backward: (cfg, parameter and gate dtype checks)."""
+    T, H = x.shape
+    dev = x.device
+    params = [t for t in (w_post, w_next) if t is not None]
+    mode = N.MOE_GATE_NONE
+    if gate is not None:
+        shapes = {(H,): N.MOE_GATE_CHANNEL, (T, 1): N.MOE_GATE_TOKEN, (T, H): N.MOE_GATE_FULL}
+        mode = shapes.get(tuple(gate.shape))
+        if mode is None:
+            raise MoeError(f"gate: shape {tuple(gate.shape)}, expected ({H},), ({T}, 1) or "
+                           f"({T}, {H})")
+        if mode == N.MOE_GATE_FULL:
+            _need(gate, "gate", x.dtype, (T, H), dev)
+        else:
+            params.append(gate)
+    pd = params[0].dtype if params else torch.float32
+    if pd not in (torch.float32, x.dtype):
+        raise MoeError(f"parameters: dtype {pd}, expected torch.float32 or {x.dtype}")
+    _opt(w_post, "w_post", pd, (H,), dev)
+    _opt(w_next, "w_next", pd, (H,), dev)
+    if gate is not None and mode != N.MOE_GATE_FULL:
+        _need(gate, "gate", pd, gate.shape, dev)
+    if y is None and (w_post is not None or gate is not None or p or w_next is None or
+                      residual_scale != 1.0):
+        raise MoeError("without y there is only the norm: w_next is required, and w_post, gate, "
+                       "p and residual_scale do not apply")
+    if p:
+        _need(rng, "rng", torch.int64, (2,), dev)
+    _opt(row_ids, "row_ids", torch.int32, (T,), dev)
+    return N.MoeNormCfg(T, int(first_row), float(p), H, _DTYPES[x.dtype], _DTYPES[pd], mode,
+                        float(eps), float(residual_scale), float(branch_scale))
+
+
+def residual_norm(x, y=None, w_post=None, gate=None, w_next=None, eps: float = 1e-6,
+                  residual_scale: float = 1.0, branch_scale: float = 1.0, p: float = 0.0,
+                  rng=None, first_row: int = 0, row_ids=None, r=None, n=None):
+    """What joins two blocks (moe_residual_norm), in one kernel:
+
+        r = residual_scale * x + branch_scale * gate * dropout(rmsnorm(y) * w_post)
+        n = rmsnorm(r) * w_next
+
+    x, y [T,H] of one type (bf16, fp16, fp32); w_post, w_next [H] and gate ([H], [T,1] or
+    [T,H]) optional; weights fp32 or of x's type, a [T,H] gate of x's type. y=None: the norm
+    before the first block. p, rng, first_row, row_ids: see dropout. r, n: outputs to write
+    (r may be x, n may be y). Returns (r, n), n None without w_next; r is x without y."""
+    _act(x, "x")
+    dev = x.device
+    if y is not None:
+        _need(y, "y", x.dtype, x.shape, dev)
+    cfg = _norm_setup(x, y, w_post, gate, w_next, eps, residual_scale, branch_scale, p, rng,
+                      first_row, row_ids)
+    if y is not None:
+        r = torch.empty_like(x) if r is None else _need(r, "r", x.dtype, x.shape, dev)
+    elif r is not None:
+        raise MoeError("without y, r is x: no output to write")
+    if w_next is not None:
+        n = torch.empty_like(x) if n is None else _need(n, "n", x.dtype, x.shape, dev)
+    elif n is not None:
+        raise MoeError("n needs w_next")
+    _rc(_call(dev, N.load().moe_residual_norm, ctypes.byref(cfg), _p(x), _p(y), _p(w_post),
+              _p(gate), _p(w_next), _p(rng), _p(row_ids), _p(r), _p(n)), "moe_residual_norm")
+    return (x if y is None else r), n
+
+
+def residual_norm_backward(r, y=None, dr=None, dn=None, w_post=None, gate=None, w_next=None,
+                           eps: float = 1e-6, residual_scale: float = 1.0,
+                           branch_scale: float = 1.0, p: float = 0.0, rng=None,
+                           first_row: int = 0, row_ids=None) -> dict:
+    """Gradients of sum(dr * r + dn * n) of residual_norm (moe_residual_norm_backward):
+    {dx, dy, dw_post, dgate, dw_next}, those that exist. r is the forward's result (x where it
+    had no y), the other arguments are the forward's; dn is given exactly with w_next, dr may
+    be None. dx, dy and a [T,H] gate's gradient have r's type, the others are fp32. The norm
+    statistics and the dropout mask are recomputed; nothing else is kept from the forward."""
+    _act(r, "r")
+    dev = r.device
+    T, H = r.shape
+    if y is not None:
+        _need(y, "y", r.dtype, r.shape, dev)
+    cfg = _norm_setup(r, y, w_post, gate, w_next, eps, residual_scale, branch_scale, p, rng,
+                      first_row, row_ids)
+    _opt(dr, "dr", r.dtype, r.shape, dev)
+    _opt(dn, "dn", r.dtype, r.shape, dev)
+    if (dn is None) != (w_next is None):
+        raise MoeError("dn is given exactly with w_next")
+    if dr is None and dn is None:
+        raise MoeError("dr or dn is required")
+    lib = N.load()
+    g = {"dx": torch.empty_like(r)}
+    if y is not None:
+        g["dy"] = torch.empty_like(r)
+    if w_post is not None:
+        g["dw_post"] = torch.empty(H, dtype=torch.float32, device=dev)
+    if gate is not None:
+        g["dgate"] = torch.empty(gate.shape, dtype=gate.dtype if cfg.gate == N.MOE_GATE_FULL
+                                 else torch.float32, device=dev)
+    if w_next is not None:
+        g["dw_next"] = torch.empty(H, dtype=torch.float32, device=dev)
+    nbytes = lib.moe_residual_norm_workspace_bytes(ctypes.byref(cfg))
+    ws = _ws(nbytes, dev, None)
+    _rc(_call(dev, lib.moe_residual_norm_backward, ctypes.byref(cfg), _p(r), _p(y), _p(w_post),
+              _p(gate), _p(w_next), _p(rng), _p(row_ids), _p(dr), _p(dn), _p(g["dx"]),
+              _p(g.get("dy")), _p(g.get("dw_post")), _p(g.get("dgate")), _p(g.get("dw_next")),
+              _p(ws), nbytes), "moe_residual_norm_backward")
+    return g
+
+
+def dropout(x, p: float, rng, first_row: int = 0, row_ids=None, out=None):
+    """Dropout of x [T,H] (bf16, fp16 or fp32) with a mask that is never stored (moe_dropout):
+    out = x / P(keep) where kept, 0 elsewhere. The mask is a function of rng (rng_state()), the
+    row and the column alone; row t is first_row + t, or row_ids[t], so a token keeps its mask
+    in any batch. The gradient is dropout(dout) with the same p, rng and rows. out may be x."""
+    _act(x, "x")
+    dev = x.device
+    _need(rng, "rng", torch.int64, (2,), dev)
+    _opt(row_ids, "row_ids", torch.int32, (x.shape[0],), dev)
+    out = torch.empty_like(x) if out is None else _need(out, "out", x.dtype, x.shape, dev)
+    _rc(_call(dev, N.load().moe_dropout, x.shape[0], x.shape[1], _DTYPES[x.dtype], float(p),
+              _p(x), _p(rng), int(first_row), _p(row_ids), _p(out)), "moe_dropout")
+    return out
+
+
 # ------------------------------------------------------------------ backward
 
 def backward_workspace(cfg: Config, dev) -> torch.Tensor:

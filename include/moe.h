@@ -385,6 +385,102 @@ MOE_API int moe_forward_train(const moe_cfg* cfg, const uint16_t* x, const uint1
                               float* logits, int32_t* topk_ids, float* topk_w, int32_t* status,
                               void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------ around the layer
+ *
+ * What joins two blocks of a residual stream: the norm after a block, its gate, dropout and
+ * residual scale, the residual sum, and the norm before the next block. Tensors as above, of
+ * the type `dtype`; H here is any multiple of 8 from 8 to 16384.
+ */
+
+/* element types */
+#define MOE_BF16 0
+#define MOE_F16 1
+#define MOE_F32 2
+
+/* gates of moe_residual_norm */
+#define MOE_GATE_NONE 0
+#define MOE_GATE_CHANNEL 1 /* [H], one value per column (a learned layer scale) */
+#define MOE_GATE_TOKEN 2   /* [T], one value per token */
+#define MOE_GATE_FULL 3    /* [T,H] */
+
+typedef struct moe_norm_cfg {
+    int64_t T;            /* rows, 0 <= T < 2^31 */
+    int64_t first_row;    /* dropout: row t is row first_row + t, 0 <= first_row, sum <= 2^32 */
+    double p;             /* dropout probability, 0 <= p <= 1 (0: none); see moe_dropout */
+    int32_t H;
+    int32_t dtype;        /* of x, y, r, n, their gradients and a MOE_GATE_FULL gate */
+    int32_t param_dtype;  /* of w_post, w_next and the other gates: MOE_F32 or `dtype` */
+    int32_t gate;         /* MOE_GATE_* */
+    float eps;            /* finite, > 0 */
+    float residual_scale; /* finite */
+    float branch_scale;   /* finite */
+} moe_norm_cfg;
+
+/*
+ *   z = drop(rms(y) * w_post)            rms(v) = v / sqrt(mean(v^2) + eps)
+ *   r = residual_scale * x + branch_scale * gate * z
+ *   n = rms(r) * w_next
+ * fp32 throughout, r and n rounded once to nearest even; n is taken from the rounded r, so
+ * the call gives the bits of two calls, one for r and one for n. A row's result depends on
+ * that row alone. Squares are summed in fp32: a row whose mean square overflows has rms 0.
+ *
+ *  x       [T,H].
+ *  y       [T,H], the block's output, or NULL: then r is x, only n is computed, and w_post,
+ *          gate and r must be NULL / MOE_GATE_NONE, residual_scale 1 and p 0.
+ *  w_post  [H] or NULL (no norm after the block).
+ *  gate    by cfg->gate, NULL for MOE_GATE_NONE.
+ *  w_next  [H] or NULL: then n must be NULL and is not computed.
+ *  rng     int64[2] device, (seed, offset), required when p > 0: read by the kernel, so a
+ *          captured graph draws new masks when its owner changes them between replays.
+ *  row_ids [T] int32 device or NULL: row t's mask is that of row row_ids[t] (taken as
+ *          unsigned), instead of first_row + t.
+ *  r       [T,H] out; may be x.   n [T,H] out; may be y.
+ */
+MOE_API int moe_residual_norm(const moe_norm_cfg* cfg, const void* x, const void* y,
+                              const void* w_post, const void* gate, const void* w_next,
+                              const int64_t* rng, const int32_t* row_ids, void* r, void* n,
+                              void* stream);
+
+/*
+ * Gradients of sum(dr * r + dn * n). The statistics and the dropout mask are recomputed:
+ * the forward keeps nothing but r and y.
+ *
+ *  r       [T,H] as the forward returned it (x where the forward had no y).
+ *  y, w_post, gate, w_next, rng, row_ids: the forward's.
+ *  dr      [T,H] or NULL (r is used by the norm alone); dn [T,H], given exactly with w_next.
+ *  dx      [T,H] out; may be dr.
+ *  dy      [T,H] out (with y).
+ *  dw_post [H], dw_next [H] fp32 out, given exactly with their weights.
+ *  dgate   out, given exactly with gate: [H] or [T] fp32, or [T,H] of `dtype`.
+ *  ws      moe_residual_norm_workspace_bytes(cfg) bytes.
+ * Parameter gradients are summed over tokens in fp32 in an order that is a function of (T, H):
+ * bitwise repeatable. T == 0 gives zeros (per-token pointers may be NULL then, here and in
+ * the forward). dx and dy of a row depend on that row alone.
+ */
+MOE_API size_t moe_residual_norm_workspace_bytes(const moe_norm_cfg* cfg);
+MOE_API int moe_residual_norm_backward(const moe_norm_cfg* cfg, const void* r, const void* y,
+                                       const void* w_post, const void* gate, const void* w_next,
+                                       const int64_t* rng, const int32_t* row_ids,
+                                       const void* dr, const void* dn, void* dx, void* dy,
+                                       float* dw_post, void* dgate, float* dw_next, void* ws,
+                                       size_t ws_bytes, void* stream);
+
+/*
+ * Dropout whose mask is never stored: out = keep ? x / P(keep) : 0, rounded once. keep is a
+ * function of (seed, offset, row, column): Philox4x32-10 with the key (seed low, seed high)
+ * and the counter (column / 8, row, offset low, offset high) gives 16 bits for each of 8
+ * columns (column 2 i of the eight in the low half of word i); an element is kept when they
+ * are at least floor(65536 p + 1/2). P(keep) is that threshold's exact probability; p below
+ * 2^-17 keeps everything. The backward is the same call on the gradient. Dropped infinities
+ * and NaNs give 0.
+ *
+ *  T, H, dtype  as in moe_norm_cfg; x [T,H], out [T,H] (may be x).
+ *  rng, first_row, row_ids as in moe_residual_norm.
+ */
+MOE_API int moe_dropout(int64_t T, int32_t H, int32_t dtype, double p, const void* x,
+                        const int64_t* rng, int64_t first_row, const int32_t* row_ids, void* out,
+                        void* stream);
+
 /* Text of a return code. */
 MOE_API const char* moe_status_string(int code);
 
