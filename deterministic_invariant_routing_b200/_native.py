@@ -29,6 +29,7 @@ MOE_ST_NAN_TOKENS = 0
 MOE_ST_ZERO_DENOM = 1
 MOE_ST_BAD_EXPERT_ID = 2
 MOE_ST_PIPE_TIMEOUT = 3
+MOE_ST_BAD_ROWS = 4
 MOE_STATUS_WORDS = 8
 
 MOE_STAGE_ROUTE = 0
@@ -38,6 +39,8 @@ MOE_STAGE_COMBINE = 3
 MOE_STAGE_FORWARD = 4
 MOE_STAGE_STATS = 5
 MOE_STAGE_BACKWARD = 6
+MOE_STAGE_MX_FFN = 7
+MOE_STAGE_MX_FORWARD = 8
 MOE_NUM_STAGE_EVENTS = 8
 
 MOE_BF16 = 0
@@ -93,6 +96,11 @@ SIGNATURES = {
     "moe_residual_norm_backward": (_I, [_NCFG] + [_P] * 15 + [_SZ, _P]),
     "moe_dropout": (_I, [_I64, ctypes.c_int32, ctypes.c_int32, ctypes.c_double, _P, _P, _I64, _P,
                          _P, _P]),
+    "moe_mx_quantize": (_I, [_I64] + [ctypes.c_int32] * 3 + [_P] * 4),
+    "moe_mx_dequantize": (_I, [_I64] + [ctypes.c_int32] * 2 + [_P] * 4),
+    "moe_mx_grouped_gemm": (_I, [_I64] + [ctypes.c_int32] * 4 + [_P] * 8),
+    "moe_mx_grouped_ffn": (_I, [_CFG] + [_P] * 15 + [_SZ, _P]),
+    "moe_mx_forward": (_I, [_CFG] + [_P] * 20 + [_SZ, _P]),
     "moe_status_string": (ctypes.c_char_p, [_I]),
     "moe_abi_version": (_I, []),
     "moe_pipeline_wait_selftest": (_I, [_P, ctypes.c_longlong, _P]),

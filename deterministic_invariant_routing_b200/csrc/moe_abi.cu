@@ -447,6 +447,131 @@ int forward_impl(const moe_cfg& c, const uint16_t* x, const uint16_t* w_router,
     return rec(ev, 7, st);
 }
 
+// scratch of moe_mx_grouped_ffn: the dispatched rows and h as codes and scales (and the
+// shared expert's)
+struct MxFfnLayout {
+    size_t xq, xs, hq, hs, tq, ts, sq, ss, total;
+};
+
+MxFfnLayout mx_ffn_layout(const moe_cfg& c)
+{
+    MxFfnLayout L{};
+    const size_t A = (size_t)c.T * c.K, T = c.I_shared ? (size_t)c.T : 0;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off += up(bytes);
+        return o;
+    };
+    L.xq = take(A * c.H / 2);
+    L.xs = take(A * c.H / 32);
+    L.hq = take(A * c.I / 2);
+    L.hs = take(A * c.I / 32);
+    L.tq = take(T * c.H / 2);
+    L.ts = take(T * c.H / 32);
+    L.sq = take(T * c.I_shared / 2);
+    L.ss = take(T * c.I_shared / 32);
+    L.total = off;
+    return L;
+}
+
+struct MxFwdLayout {
+    size_t logits, ids, w, offsets, perm_token, dest_row, perm_ws, y, y_s, ffn, total;
+};
+
+MxFwdLayout mx_fwd_layout(const moe_cfg& c)
+{
+    MxFwdLayout L{};
+    const size_t A = (size_t)c.T * c.K;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off += up(bytes);
+        return o;
+    };
+    L.logits = take((size_t)c.T * c.E * 4);
+    L.ids = take(A * 4);
+    L.w = take(A * 4);
+    L.offsets = take((size_t)(c.E + 1) * 4);
+    L.perm_token = take(A * 4);
+    L.dest_row = take(A * 4);
+    L.perm_ws = take(permute_ws_bytes(c));
+    L.y = take(A * c.H * 2);
+    L.y_s = take(c.I_shared ? (size_t)c.T * c.H * 2 : 0);
+    L.ffn = take(mx_ffn_layout(c).total);
+    L.total = off;
+    return L;
+}
+
+// weights of 4-bit experts
+struct MxExperts {
+    const uint8_t *w13, *w13_sc, *w2, *w2_sc, *w13_s, *w13_s_sc, *w2_s, *w2_s_sc;
+};
+
+int check_mx_experts(const moe_cfg& c, const MxExperts& w)
+{
+    for (const uint8_t* p : {w.w13, w.w13_sc, w.w2, w.w2_sc})
+        if (p == nullptr || !aligned16(p)) return MOE_ERR_ARG;
+    if (c.I_shared > 0)
+        for (const uint8_t* p : {w.w13_s, w.w13_s_sc, w.w2_s, w.w2_s_sc})
+            if (p == nullptr || !aligned16(p)) return MOE_ERR_ARG;
+    return MOE_OK;
+}
+
+// gate_up with SwiGLU to quantised h, then down, over rows given as codes and scales
+cudaError_t mx_experts(const uint8_t* xq, const uint8_t* xs, int64_t rows, const int32_t* offsets,
+                       int groups, int H, int I, const uint8_t* w13, const uint8_t* w13_sc,
+                       const uint8_t* w2, const uint8_t* w2_sc, uint8_t* hq, uint8_t* hs,
+                       uint16_t* y, int32_t* status, cudaStream_t st)
+{
+    MxProblem p{};
+    p.a = xq;
+    p.a_scales = xs;
+    p.rows = rows;
+    p.offsets = offsets;
+    p.groups = groups;
+    p.b = w13;
+    p.b_scales = w13_sc;
+    p.k = H;
+    p.n = I;
+    p.swiglu = true;
+    p.out_codes = hq;
+    p.out_scales = hs;
+    p.status = status;
+    const cudaError_t e = launch_mx_gemm(p, st);
+    if (e != cudaSuccess) return e;
+    p.a = hq;
+    p.a_scales = hs;
+    p.b = w2;
+    p.b_scales = w2_sc;
+    p.k = I;
+    p.n = H;
+    p.swiglu = false;
+    p.out = y;
+    p.out_codes = p.out_scales = nullptr;
+    return launch_mx_gemm(p, st);
+}
+
+int mx_ffn_impl(const moe_cfg& c, const uint16_t* x, const int32_t* dest_row,
+                const int32_t* offsets, const MxExperts& w, uint16_t* y, uint16_t* y_shared,
+                int32_t* status, void* ws, cudaStream_t st)
+{
+    const MxFfnLayout L = mx_ffn_layout(c);
+    const bool shared = c.I_shared > 0;
+    uint8_t *xq = at<uint8_t>(ws, L.xq), *xs = at<uint8_t>(ws, L.xs);
+    uint8_t* tq = shared ? at<uint8_t>(ws, L.tq) : nullptr;
+    uint8_t* ts = shared ? at<uint8_t>(ws, L.ts) : nullptr;
+    int rc = cuda_rc(launch_mx_scatter(c, x, dest_row, xq, xs, tq, ts, status, st));
+    if (rc != MOE_OK) return rc;
+    rc = cuda_rc(mx_experts(xq, xs, (int64_t)c.T * c.K, offsets, c.E, c.H, c.I, w.w13, w.w13_sc,
+                            w.w2, w.w2_sc, at<uint8_t>(ws, L.hq), at<uint8_t>(ws, L.hs), y, status,
+                            st));
+    if (rc != MOE_OK || !shared) return rc;
+    return cuda_rc(mx_experts(tq, ts, c.T, nullptr, 1, c.H, c.I_shared, w.w13_s, w.w13_s_sc,
+                              w.w2_s, w.w2_s_sc, at<uint8_t>(ws, L.sq), at<uint8_t>(ws, L.ss),
+                              y_shared, status, st));
+}
+
 // Token chunks of moe_forward_host for a nominal chunk C: up to 2 C tokens in chunks of at
 // most C (equal sizes); beyond that a first and a last chunk of C / 2 -- the pipeline's fill
 // (the first copy in) and drain (the last copy out) are only as long as those -- and the
@@ -830,6 +955,8 @@ MOE_API size_t moe_workspace_bytes(const moe_cfg* cfg, int stage)
         case MOE_STAGE_FORWARD: return fwd_layout(*cfg).total;
         case MOE_STAGE_STATS: return stats_ws_bytes(*cfg);
         case MOE_STAGE_BACKWARD: return bwd_layout(*cfg).total;
+        case MOE_STAGE_MX_FFN: return mx_ffn_layout(*cfg).total;
+        case MOE_STAGE_MX_FORWARD: return mx_fwd_layout(*cfg).total;
         default: return 0;
     }
 }
@@ -1239,6 +1366,144 @@ MOE_API int moe_dropout(int64_t T, int32_t H, int32_t dtype, double p, const voi
     if ((rc = check_device()) != MOE_OK) return rc;
     return cuda_rc(launch_dropout(T, H, dtype, p, x, rng, first_row, row_ids, out,
                                   static_cast<cudaStream_t>(stream)));
+}
+
+MOE_API int moe_mx_quantize(int64_t rows, int32_t K, int32_t dtype, int32_t tiled, const void* x,
+                            uint8_t* codes, uint8_t* scales, void* stream)
+{
+    if (rows < 0 || K < 32 || K > (1 << 20) || K % 32 != 0 || rows >= ((int64_t)1 << 42) / K)
+        return MOE_ERR_SHAPE;
+    if (dtype != MOE_BF16 && dtype != MOE_F16 && dtype != MOE_F32) return MOE_ERR_SHAPE;
+    if (tiled != 0 && tiled != 1) return MOE_ERR_ARG;
+    if (tiled && (rows % 128 != 0 || K % 128 != 0)) return MOE_ERR_SHAPE;
+    if (rows == 0) return MOE_OK;
+    if (x == nullptr || codes == nullptr || scales == nullptr) return MOE_ERR_ARG;
+    int rc;
+    if ((rc = check_aligned({x, codes})) != MOE_OK) return rc;
+    if ((rc = check_device()) != MOE_OK) return rc;
+    return cuda_rc(launch_mx_quantize(rows, K, dtype, tiled != 0, x, codes, scales,
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+MOE_API int moe_mx_dequantize(int64_t rows, int32_t K, int32_t dtype, const uint8_t* codes,
+                              const uint8_t* scales, void* out, void* stream)
+{
+    if (rows < 0 || K < 32 || K > (1 << 20) || K % 32 != 0 || rows >= ((int64_t)1 << 42) / K)
+        return MOE_ERR_SHAPE;
+    if (dtype != MOE_BF16 && dtype != MOE_F16 && dtype != MOE_F32) return MOE_ERR_SHAPE;
+    if (rows == 0) return MOE_OK;
+    if (codes == nullptr || scales == nullptr || out == nullptr) return MOE_ERR_ARG;
+    int rc;
+    if ((rc = check_aligned({codes, out})) != MOE_OK) return rc;
+    if ((rc = check_device()) != MOE_OK) return rc;
+    return cuda_rc(launch_mx_dequantize(rows, K, dtype, codes, scales, out,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+MOE_API int moe_mx_grouped_gemm(int64_t rows, int32_t K, int32_t N, int32_t groups,
+                                int32_t swiglu, const uint8_t* a_codes, const uint8_t* a_scales,
+                                const int32_t* offsets, const uint8_t* b_codes,
+                                const uint8_t* b_scales, uint16_t* out, int32_t* status,
+                                void* stream)
+{
+    if (swiglu != 0 && swiglu != 1) return MOE_ERR_ARG;
+    const int unit = swiglu ? 256 : 128;
+    if (rows < 0 || rows >= ((int64_t)1 << 31) || groups < 1 || groups > 1024 || K < 128 ||
+        K > 32768 || K % 128 != 0 || N < unit || N > 256 * unit || N % unit != 0)
+        return MOE_ERR_SHAPE;
+    // rows of B are 32-bit coordinates
+    if ((int64_t)groups * N >= ((int64_t)1 << 31) / 2) return MOE_ERR_SHAPE;
+    if (offsets == nullptr && groups != 1) return MOE_ERR_ARG;
+    if (rows == 0) return MOE_OK;
+    int rc;
+    for (const void* p : std::initializer_list<const void*>{a_codes, a_scales, b_codes, b_scales, out})
+        if (p == nullptr || !aligned16(p)) return MOE_ERR_ARG;
+    if ((rc = check_device()) != MOE_OK) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (status && (rc = cuda_rc(cudaMemsetAsync(status, 0, MOE_STATUS_WORDS * 4, st))) != MOE_OK)
+        return rc;
+    MxProblem p{};
+    p.a = a_codes;
+    p.a_scales = a_scales;
+    p.rows = rows;
+    p.offsets = offsets;
+    p.groups = groups;
+    p.b = b_codes;
+    p.b_scales = b_scales;
+    p.k = K;
+    p.n = swiglu ? N / 2 : N;
+    p.swiglu = swiglu != 0;
+    p.out = out;
+    p.status = status;
+    return cuda_rc(launch_mx_gemm(p, st));
+}
+
+MOE_API int moe_mx_grouped_ffn(const moe_cfg* cfg, const uint16_t* x, const int32_t* dest_row,
+                               const int32_t* offsets, const uint8_t* w13_codes,
+                               const uint8_t* w13_scales, const uint8_t* w2_codes,
+                               const uint8_t* w2_scales, const uint8_t* w13_s_codes,
+                               const uint8_t* w13_s_scales, const uint8_t* w2_s_codes,
+                               const uint8_t* w2_s_scales, uint16_t* y, uint16_t* y_shared,
+                               int32_t* status, void* ws, size_t ws_bytes, void* stream)
+{
+    int rc = check_cfg(cfg);
+    if (rc != MOE_OK || cfg->T == 0) return rc;
+    const MxExperts w{w13_codes, w13_scales, w2_codes, w2_scales,
+                      w13_s_codes, w13_s_scales, w2_s_codes, w2_s_scales};
+    if ((rc = check_mx_experts(*cfg, w)) != MOE_OK) return rc;
+    if (x == nullptr || dest_row == nullptr || offsets == nullptr || y == nullptr ||
+        (cfg->I_shared > 0 && y_shared == nullptr))
+        return MOE_ERR_ARG;
+    if ((rc = check_aligned({x, y, y_shared})) != MOE_OK) return rc;
+    if (ws == nullptr || !aligned16(ws) || ws_bytes < mx_ffn_layout(*cfg).total)
+        return MOE_ERR_WORKSPACE;
+    if ((rc = check_device()) != MOE_OK) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (status && (rc = cuda_rc(cudaMemsetAsync(status, 0, MOE_STATUS_WORDS * 4, st))) != MOE_OK)
+        return rc;
+    return mx_ffn_impl(*cfg, x, dest_row, offsets, w, y, y_shared, status, ws, st);
+}
+
+MOE_API int moe_mx_forward(const moe_cfg* cfg, const uint16_t* x, const uint16_t* w_router,
+                           const float* logit_bias, const float* sel_bias,
+                           const uint8_t* token_mask, const uint8_t* w13_codes,
+                           const uint8_t* w13_scales, const uint8_t* w2_codes,
+                           const uint8_t* w2_scales, const uint8_t* w13_s_codes,
+                           const uint8_t* w13_s_scales, const uint8_t* w2_s_codes,
+                           const uint8_t* w2_s_scales, uint16_t* out, float* logits,
+                           int32_t* topk_ids, float* topk_w, int32_t* offsets, int32_t* status,
+                           void* ws, size_t ws_bytes, void* stream)
+{
+    int rc = check_cfg(cfg);
+    if (rc != MOE_OK || cfg->T == 0) return rc;
+    const moe_cfg& c = *cfg;
+    const MxExperts w{w13_codes, w13_scales, w2_codes, w2_scales,
+                      w13_s_codes, w13_s_scales, w2_s_codes, w2_s_scales};
+    if ((rc = check_mx_experts(c, w)) != MOE_OK) return rc;
+    if (x == nullptr || w_router == nullptr || out == nullptr || status == nullptr)
+        return MOE_ERR_ARG;
+    if ((rc = check_aligned({x, w_router, out})) != MOE_OK) return rc;
+    const MxFwdLayout L = mx_fwd_layout(c);
+    if (ws == nullptr || !aligned16(ws) || ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    if ((rc = check_device()) != MOE_OK) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if ((rc = cuda_rc(cudaMemsetAsync(status, 0, MOE_STATUS_WORDS * 4, st))) != MOE_OK) return rc;
+    float* lg = logits ? logits : at<float>(ws, L.logits);
+    int32_t* ids = topk_ids ? topk_ids : at<int32_t>(ws, L.ids);
+    float* tw = topk_w ? topk_w : at<float>(ws, L.w);
+    int32_t* offs = offsets ? offsets : at<int32_t>(ws, L.offsets);
+    int32_t* dest = at<int32_t>(ws, L.dest_row);
+    uint16_t* y = at<uint16_t>(ws, L.y);
+    uint16_t* y_s = c.I_shared > 0 ? at<uint16_t>(ws, L.y_s) : nullptr;
+    if ((rc = router_and_route(c, x, w_router, logit_bias, sel_bias, token_mask, lg, ids, tw,
+                               status, nullptr, st)) != MOE_OK)
+        return rc;
+    rc = cuda_rc(launch_permute(c, ids, offs, at<int32_t>(ws, L.perm_token), dest, status,
+                                at<void>(ws, L.perm_ws), st));
+    if (rc != MOE_OK) return rc;
+    rc = mx_ffn_impl(c, x, dest, offs, w, y, y_s, status, at<void>(ws, L.ffn), st);
+    if (rc != MOE_OK) return rc;
+    return cuda_rc(launch_combine(c, y, tw, dest, y_s, token_mask, out, st));
 }
 
 }  // extern "C"

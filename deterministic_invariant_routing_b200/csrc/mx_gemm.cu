@@ -1,0 +1,620 @@
+// The expert products with both operands in the microscaled 4-bit format: rows of A grouped by
+// expert, A and B as e2m1 codes under e8m0 scales (mx_format.cuh),
+//
+//   out[r, c] = sum over k of (A[r, k] 2^(sa[r, k / 32] - 127)) (B_g[c, k] 2^(sb[c, k / 32] - 127))
+//
+// on the tensor cores with tcgen05.mma kind::mxf4 (K = 64 an instruction, the scales applied
+// by the tensor core, fp32 accumulation in TMEM). The structure is the bf16 pair kernel's: a
+// cluster of two CTAs computes 256 rows by 256 columns, each CTA holding its 128 rows of A and
+// half of B's columns, so that a k-block (256 columns of K: 128 bytes a row) takes 32 KiB a CTA
+// for the 512 cycles its four instructions need.
+//
+// Scales: an instruction reads them from TMEM, 4 bytes (4 blocks of 32) per row in a 32-bit
+// column for every 32 rows. They are staged beside the operands and copied in by tcgen05.cp
+// (32x128b.warpx4: 512 bytes of shared memory, 128 rows by 4 blocks, to 4 columns), issued in
+// order before the instructions that read them:
+//   B: stored in exactly those tiles (the layout weights are kept in), loaded by TMA; each CTA
+//      needs the scales of all 256 columns.
+//   A: rows start anywhere (an expert's first row is not a multiple of 128), so a warp reads
+//      them from the row-major array, four rows a lane -- the lane's 16 bytes of a tile -- a few
+//      k-blocks ahead, and writes them to shared memory itself.
+//
+// Arithmetic per row: k-blocks in increasing order, four K = 64 steps each (two in a last block
+// of 128 columns), one accumulator; nothing depends on where the row sits, on its expert's
+// other rows or on T. Rows past the group's end are computed and never stored.
+//
+// Every wait is bounded (MOE_ST_PIPE_TIMEOUT); offsets outside [0, rows] are clamped and counted
+// in MOE_ST_BAD_ROWS, so no tile reaches past the buffers.
+#include "mx_format.cuh"
+#include "tc_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int XM = 256;                 // rows per pair tile
+constexpr int XH = 128;                 // rows per CTA
+constexpr int XN = 256;                 // columns per pair tile (SwiGLU: 128 gate, 128 up)
+constexpr int XK = 256;                 // columns of K per stage
+constexpr uint32_t kXA = XH * XK / 2;   // 16 KiB
+constexpr uint32_t kXB = XH * XK / 2;   // 16 KiB: this CTA's half of the columns
+constexpr uint32_t kXSA = 1024;         // scales of 128 rows, two tiles of 4 blocks
+constexpr uint32_t kXSB = 2048;         // scales of 256 columns
+constexpr uint32_t kXStage = kXA + kXB + kXSA + kXSB;
+constexpr int kXS = 5;                  // stages
+constexpr int kXEpiWarps = 8;
+constexpr uint32_t kXEpi = kXEpiWarps * 2 * 2048;
+constexpr int kXThreads = 32 * (2 + kXEpiWarps + 1);
+constexpr int kXBars = 2 * kXS + 3;
+constexpr uint32_t kXCols = 512;        // TMEM columns: the accumulator, then the scales
+constexpr uint32_t kXTmemSA = 256, kXTmemSB = 264;
+constexpr uint16_t kXPair = 0x3;
+constexpr int kXAhead = 4;              // k-blocks the A scales are read ahead
+
+enum MxEpilogue { MX_BF16 = 0, MX_SWIGLU = 1, MX_SWIGLU_QUANT = 2 };
+
+struct MxArgs {
+    int k, k_blocks, n, n_tiles, groups;
+    int64_t rows;
+    const int32_t* offsets;  // [groups + 1], or NULL: one group of all rows
+    const uint8_t* a_scales; // [rows, k / 32]
+    int sb_tiles;            // 128-row scale tiles per group of B
+    int half;                // SwiGLU: n, the first up row; 0 otherwise
+    uint16_t* out;           // [rows, n] bf16
+    uint8_t* out_codes;      // MX_SWIGLU_QUANT: [rows, n / 2] and [rows, n / 32]
+    uint8_t* out_scales;
+    int32_t* status;
+};
+
+struct MxTile {
+    int g, n;
+    int64_t row0, row_end;
+};
+
+// kind::mxf4 with e2m1 operands (format 1), e8m0 scales (bit 23), M = 256, N = 256, both K-major;
+// the scale bytes of a 32-bit column that the instruction reads start at byte `id` (0 or 2)
+constexpr uint32_t mx_idesc(int m, int n, uint32_t id)
+{
+    return (id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) |
+           ((uint32_t)(m >> 4) << 24) | (id << 29);
+}
+
+__device__ __forceinline__ void mma_mxf4_pair(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc,
+                                              uint32_t sa, uint32_t sb, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}\n" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+}
+
+// 512 bytes of both CTAs' shared memory (32 rows of 16) to 4 TMEM columns, in all lane quarters
+__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t desc)
+{
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                 : "memory");
+}
+
+// descriptor of such a 512-byte tile: no swizzle, groups of 8 rows 128 bytes apart
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr)
+{
+    return (uint64_t)((saddr >> 4) & 0x3fffu) | (uint64_t)(128u >> 4) << 32 | (uint64_t)1u << 46;
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(kXThreads, 1)
+    mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ CUtensorMap tmSB,
+                   const __grid_constant__ CUtensorMap tmO, MxArgs args)
+{
+    constexpr bool kGlu = MODE != MX_BF16;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_s = smem_u32(smem_raw);
+    uint8_t* base = smem_raw + ((1024u - (raw_s & 1023u)) & 1023u);
+    const uint32_t sA0 = smem_u32(base);
+    const uint32_t sB0 = sA0 + kXS * kXA;
+    const uint32_t sSA0 = sB0 + kXS * kXB;
+    const uint32_t sSB0 = sSA0 + kXS * kXSA;
+    const uint32_t sE0 = sA0 + kXS * kXStage;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(base + kXS * kXStage + kXEpi);
+    const uint32_t bar0 = smem_u32(bars);
+    auto full_bar = [&](int s) { return bar0 + 8u * (uint32_t)s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (uint32_t)(kXS + s); };
+    const uint32_t tfull = bar0 + 8u * (uint32_t)(2 * kXS);
+    const uint32_t tempty = tfull + 8u, drain = tfull + 16u;
+    uint32_t* misc = reinterpret_cast<uint32_t*>(bars + kXBars);  // [0] tmem, [1] abort
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+    int32_t* prefix = reinterpret_cast<int32_t*>(misc + 4);  // [groups + 1] row tiles before g
+    int32_t* offs = prefix + (args.groups + 1);              // [groups + 1]
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = args.groups;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kXS; ++s) {
+            mbar_init(full_bar(s), 3);  // the leader's byte count, each CTA's A scales
+            mbar_init(empty_bar(s), 1);
+        }
+        mbar_init(tfull, 1);
+        mbar_init(tempty, 2 * kXEpiWarps * 32);
+        mbar_init(drain, 1);
+        misc[1] = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc_pair(smem_u32(misc), kXCols);
+    pdl_wait();
+    if (warp == 2) {
+        bool bad = false;
+        auto row_off = [&](int g) -> int {
+            if (args.offsets == nullptr) return g == 0 ? 0 : (int)args.rows;
+            const int o = args.offsets[g];
+            if (o < 0 || o > args.rows) bad = true;
+            return o < 0 ? 0 : (o > args.rows ? (int)args.rows : o);
+        };
+        auto tiles_of = [&](int n) -> int {
+            if (n < 0) bad = true;
+            return n > 0 ? (n + XM - 1) / XM : 0;
+        };
+        const int per = (G + 31) / 32;
+        const int beg = lane * per < G ? lane * per : G;
+        const int end = beg + per < G ? beg + per : G;
+        int sum = 0;
+        for (int g = beg; g < end; ++g) {
+            const int r0 = row_off(g);
+            offs[g] = r0;
+            sum += tiles_of(row_off(g + 1) - r0);
+        }
+        if (lane == 0) offs[G] = row_off(G);
+        int incl = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += o;
+        }
+        int run = incl - sum;
+        for (int g = beg; g < end; ++g) {
+            prefix[g] = run;
+            run += tiles_of(row_off(g + 1) - row_off(g));
+        }
+        if (lane == 31) prefix[G] = incl;
+        if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0)
+            status_add(args.status, MOE_ST_BAD_ROWS, 1);
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = misc[0];
+    const int total = prefix[G] * args.n_tiles;
+    auto decode = [&](int t) -> MxTile {
+        MxTile ti;
+        const int mt = t / args.n_tiles;
+        ti.n = t - mt * args.n_tiles;
+        int lo = 0, hi = G - 1;
+        while (lo < hi) {  // the last group with prefix[g] <= mt: empty groups have no tile
+            const int mid = (lo + hi + 1) >> 1;
+            if (prefix[mid] <= mt) lo = mid;
+            else hi = mid - 1;
+        }
+        ti.g = lo;
+        ti.row0 = (int64_t)offs[lo] + (int64_t)(mt - prefix[lo]) * XM;
+        ti.row_end = offs[lo + 1];
+        return ti;
+    };
+
+    if (warp == 0) {
+        // -------------------------------------------------------------- TMA producer
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, armed = 0, armed_phase = 0;
+            const uint32_t fb0 = mapa_shared(full_bar(0), 0);
+            const int kc = args.k / 128;  // scale tiles along K
+            for (int t = cluster; t < total && !*abort_flag; t += nclusters) {
+                const MxTile ti = decode(t);
+                const int arow = (int)ti.row0 + (int)rank * XH;
+                const int b0 = ti.g * args.sb_tiles + (kGlu ? ti.n : 2 * ti.n);  // 128-row tiles
+                const int b1 = kGlu ? b0 + args.half / 128 : b0 + 1;
+                const int brow = (leader ? b0 : b1) * 128;
+                bool ok = true;
+                for (int kb = 0; kb < args.k_blocks; ++kb) {
+                    if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = fb0 + 8u * (uint32_t)stage;
+                    if (leader) mbar_expect_tx(full_bar(stage), 2 * (kXA + kXB + kXSB));
+                    const uint32_t ss = (uint32_t)stage;
+                    tma_load_2d_pair(sA0 + ss * kXA, &tmA, kb * (XK / 2), arow, fb);
+                    tma_load_2d_pair(sB0 + ss * kXB, &tmB, kb * (XK / 2), brow, fb);
+                    tma_load_2d_pair(sSB0 + ss * kXSB, &tmSB, 0, b0 * kc + 2 * kb, fb);
+                    tma_load_2d_pair(sSB0 + ss * kXSB + 1024u, &tmSB, 0, b1 * kc + 2 * kb, fb);
+                    armed |= 1u << stage;
+                    armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
+                    if (++stage == kXS) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+            }
+            pdl_trigger();
+            if (*abort_flag && leader) {
+                for (int s = 0; s < kXS; ++s)
+                    if (armed & (1u << s))
+                        wait_bounded(full_bar(s), (armed_phase >> s) & 1u, abort_flag,
+                                     args.status, false);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            // ---------------------------------------------------------- MMA issuer
+            const uint64_t ad0 = sw128_desc(sA0), bd0 = sw128_desc(sB0);
+            const uint64_t sad0 = scale_desc(sSA0), sbd0 = scale_desc(sSB0);
+            const uint32_t tsa = tmem_base + kXTmemSA, tsb = tmem_base + kXTmemSB;
+            int stage = 0;
+            uint32_t phase = 0;
+            int i = 0;
+            for (int t = cluster; t < total && !*abort_flag; t += nclusters, ++i) {
+                if (!wait_bounded(tempty, ((uint32_t)i & 1u) ^ 1u, abort_flag, args.status)) break;
+                tc_fence_after();
+                bool ok = true;
+                for (int kb = 0; kb < args.k_blocks; ++kb) {
+                    if (!wait_bounded(full_bar(stage), phase, abort_flag, args.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t st = (uint64_t)(uint32_t)stage;
+                    const uint64_t ad = ad0 + st * (kXA >> 4), bd = bd0 + st * (kXB >> 4);
+                    const uint64_t sad = sad0 + st * (kXSA >> 4), sbd = sbd0 + st * (kXSB >> 4);
+                    const int chunks = args.k - kb * XK >= XK ? 2 : 1;  // of 128 columns
+                    for (int c = 0; c < chunks; ++c) {
+                        tmem_cp_scales_pair(tsa + 4u * c, sad + (uint64_t)(c * (512 >> 4)));
+                        tmem_cp_scales_pair(tsb + 8u * c, sbd + (uint64_t)(c * (512 >> 4)));
+                        tmem_cp_scales_pair(tsb + 8u * c + 4u,
+                                            sbd + (uint64_t)((1024 + c * 512) >> 4));
+                    }
+                    for (int c = 0; c < chunks; ++c) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint64_t step = (uint64_t)(2 * (2 * c + h));
+                            mma_mxf4_pair(tmem_base, ad + step, bd + step,
+                                          h ? mx_idesc(XM, XN, 2) : mx_idesc(XM, XN, 0),
+                                          tsa + 4u * c, tsb + 8u * c,
+                                          (kb | c | h) != 0 ? 1u : 0u);
+                        }
+                    }
+                    mma_commit_pair_mc(empty_bar(stage), kXPair);
+                    if (++stage == kXS) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                mma_commit_pair_mc(tfull, kXPair);
+            }
+            mma_commit_pair(drain);
+            wait_bounded(drain, 0u, abort_flag, args.status, false);
+        }
+    } else if (warp == 2 + kXEpiWarps) {
+        // -------------------------------------------------------------- A scales
+        // lane l holds rows l, l + 32, l + 64, l + 96 of this CTA's 128: bytes 16 l .. of a tile
+        const int blocks = args.k / 32;
+        const bool wide = args.k % 256 == 0;  // a row's 8 scales of a k-block are 8-byte aligned
+        const uint32_t fb0 = mapa_shared(full_bar(0), 0);
+        int it = cluster, ikb = 0;  // the k-block to read next
+        const uint8_t* src[4] = {nullptr, nullptr, nullptr, nullptr};
+        auto rows_of = [&](int t) {
+            if (t >= total) return;
+            const MxTile ti = decode(t);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t r = ti.row0 + (int64_t)rank * XH + 32 * j + lane;
+                src[j] = r < ti.row_end ? args.a_scales + r * blocks : nullptr;
+            }
+        };
+        auto read = [&](uint2 (&b)[4]) {
+            if (it >= total) return;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                b[j] = make_uint2(0u, 0u);
+                if (src[j] != nullptr) {
+                    const uint8_t* p = src[j] + ikb * 8;
+                    if (wide) {
+                        b[j] = *reinterpret_cast<const uint2*>(p);
+                    } else {
+                        b[j].x = *reinterpret_cast<const uint32_t*>(p);
+                        if (ikb * 8 + 4 < blocks) b[j].y = *reinterpret_cast<const uint32_t*>(p + 4);
+                    }
+                }
+            }
+            if (++ikb == args.k_blocks) {
+                ikb = 0;
+                it += nclusters;
+                rows_of(it);
+            }
+        };
+        uint2 buf[kXAhead][4];
+        rows_of(it);
+#pragma unroll
+        for (int d = 0; d < kXAhead; ++d) read(buf[d]);
+        int t = cluster, kb = 0, stage = 0;
+        uint32_t phase = 0;
+        bool run = t < total;
+        while (run) {
+#pragma unroll
+            for (int d = 0; d < kXAhead; ++d) {
+                if (run) {
+                    int ok = 1;
+                    if (lane == 0)
+                        ok = wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.status);
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) {
+                        run = false;
+                    } else {
+                        const uint32_t dst = sSA0 + (uint32_t)stage * kXSA + (uint32_t)lane * 16u;
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst),
+                                     "r"(buf[d][0].x), "r"(buf[d][1].x), "r"(buf[d][2].x),
+                                     "r"(buf[d][3].x)
+                                     : "memory");
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 512u),
+                                     "r"(buf[d][0].y), "r"(buf[d][1].y), "r"(buf[d][2].y),
+                                     "r"(buf[d][3].y)
+                                     : "memory");
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(fb0 + 8u * (uint32_t)stage);
+                        read(buf[d]);
+                        if (++stage == kXS) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                        if (++kb == args.k_blocks) {
+                            kb = 0;
+                            t += nclusters;
+                            run = t < total;
+                        }
+                    }
+                }
+            }
+        }
+    } else {
+        // -------------------------------------------------------------- epilogue
+        const int q = warp & 3;  // TMEM lanes 32 q .. 32 q + 31
+        const int row = q * 32 + lane;
+        const int c0 = 32 * ((warp - 2) >> 2);  // this warp's first 32-column chunk, then + 64
+        const uint32_t tempty_leader = mapa_shared(tempty, 0);
+        const uint32_t ebuf = sE0 + (uint32_t)(warp - 2) * 4096u;
+        uint32_t eb = 0;
+        const uint32_t erow = (uint32_t)lane * 64u, eswz = ((uint32_t)lane >> 1) & 3u;
+        auto store_block = [&](const uint32_t (&pk)[16], bool full_blk, bool valid, int row_blk,
+                               int col, uint16_t* dst_row) {
+            if (full_blk) {
+                const uint32_t b = ebuf + eb * 2048u;
+                if (lane == 0) bulk_wait_read<1>();
+                __syncwarp();
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     b + erow + ((((uint32_t)v) ^ eswz) << 4)),
+                                 "r"(pk[4 * v]), "r"(pk[4 * v + 1]), "r"(pk[4 * v + 2]),
+                                 "r"(pk[4 * v + 3])
+                                 : "memory");
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_2d(&tmO, b, col, row_blk);
+                    bulk_commit();
+                }
+                eb ^= 1u;
+            } else if (valid) {
+                uint4* dst = reinterpret_cast<uint4*>(dst_row);
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    dst[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+            }
+        };
+        int i = 0;
+        for (int t = cluster; t < total && !*abort_flag; t += nclusters, ++i) {
+            const MxTile ti = decode(t);
+            int ok = 1;
+            if (lane == 0) ok = wait_bounded(tfull, (uint32_t)i & 1u, abort_flag, args.status);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16);
+            const int64_t grow = ti.row0 + (int64_t)rank * XH + row;
+            const bool valid = grow < ti.row_end;
+            const int row_blk = (int)(ti.row0 + (int64_t)rank * XH + q * 32);
+            const bool full_blk = (int64_t)row_blk + 31 < ti.row_end;
+            if (kGlu) {
+#pragma unroll 1
+                for (int c = c0; c < XN / 2; c += 64) {
+                    uint32_t g[32], u[32];
+                    tmem_ld32(tbase + (uint32_t)c, g);
+                    tmem_ld32(tbase + (uint32_t)(XN / 2 + c), u);
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float hv[2];
+#pragma unroll
+                        for (int h2 = 0; h2 < 2; ++h2)
+                            hv[h2] = swiglu(__uint_as_float(g[2 * j + h2]),
+                                            __uint_as_float(u[2 * j + h2]));
+                        pk[j] = bf16x2_rne(hv[0], hv[1]);
+                    }
+                    const int col = ti.n * (XN / 2) + c;
+                    if (MODE == MX_SWIGLU) {
+                        store_block(pk, full_blk, valid, row_blk, col,
+                                    args.out + grow * args.n + col);
+                    } else if (valid) {
+                        // 32 columns of a row are one block: quantised from the bf16 values, so
+                        // the fused product gives the codes of the two calls it replaces
+                        uint32_t m = 0;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            m = max(m, max(pk[j] << 16 & 0x7fffffffu, pk[j] & 0x7fff0000u));
+                        const uint32_t s = mx_scale_byte(m);
+                        uint32_t code[4];
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            float f[8];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                f[2 * e] = __uint_as_float(pk[4 * v + e] << 16);
+                                f[2 * e + 1] = __uint_as_float(pk[4 * v + e] & 0xffff0000u);
+                            }
+                            code[v] = mx_encode8(f, s);
+                        }
+                        *reinterpret_cast<uint4*>(args.out_codes + grow * (args.n / 2) + col / 2) =
+                            make_uint4(code[0], code[1], code[2], code[3]);
+                        args.out_scales[grow * (args.n / 32) + col / 32] = (uint8_t)s;
+                    }
+                }
+            } else {
+#pragma unroll 1
+                for (int c = c0; c < XN; c += 64) {
+                    const int col = ti.n * XN + c;
+                    if (col >= args.n) break;  // past the last column (n a multiple of 128)
+                    uint32_t r[32];
+                    tmem_ld32(tbase + (uint32_t)c, r);
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        pk[j] = bf16x2_rne(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                    store_block(pk, full_blk, valid, row_blk, col, args.out + grow * args.n + col);
+                }
+            }
+            tc_fence_before();
+            mbar_arrive_cluster(tempty_leader);
+        }
+        if (lane == 0) bulk_wait_all();
+    }
+
+    tc_fence_before();
+    cluster_sync();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, kXCols);
+    }
+}
+
+// codes [rows, k / 2] bytes: boxes of 128 bytes by box_rows rows, 128-byte swizzle
+bool make_codes_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t k, int box_rows)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)(k / 2), (cuuint64_t)(rows > 0 ? rows : 1)};
+    cuuint64_t strides[1] = {(cuuint64_t)(k / 2)};
+    cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// scale tiles of 512 bytes, two (256 columns of K) a box
+bool make_scale_map(CUtensorMap* m, const void* ptr, int64_t tiles)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[2] = {256, (cuuint64_t)tiles};
+    cuuint64_t strides[1] = {512};
+    cuuint32_t box[2] = {256, 2};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(ptr), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE>
+cudaError_t launch_mode(const MxProblem& p, cudaStream_t st)
+{
+    auto kernel = mx_gemm_kernel<MODE>;
+    const size_t smem = 1024 + (size_t)kXS * kXStage + kXEpi + kXBars * 8 + 16 +
+                        (size_t)2 * (p.groups + 1) * sizeof(int32_t);
+    if (smem > 232448) return cudaErrorInvalidValue;
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    static bool attr_set[64] = {};
+    if (!attr_set[dev]) {
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+        if (err != cudaSuccess) return err;
+        attr_set[dev] = true;
+    }
+    const bool glu = MODE != MX_BF16;
+    const int b_rows = glu ? 2 * p.n : p.n;
+    CUtensorMap ma, mb, ms, mo;
+    if (!make_codes_map(&ma, p.a, p.rows, p.k, XH)) return cudaErrorInvalidValue;
+    if (!make_codes_map(&mb, p.b, (int64_t)p.groups * b_rows, p.k, XH)) return cudaErrorInvalidValue;
+    if (!make_scale_map(&ms, p.b_scales, (int64_t)p.groups * (b_rows / 128) * (p.k / 128)))
+        return cudaErrorInvalidValue;
+    if (MODE == MX_SWIGLU_QUANT) mo = ma;  // stored from registers: the map is not used
+    else if (!make_store_map(&mo, p.out, p.rows, p.n, p.n)) return cudaErrorInvalidValue;
+    MxArgs a{};
+    a.k = p.k;
+    a.k_blocks = (p.k + XK - 1) / XK;
+    a.n = p.n;
+    a.n_tiles = glu ? p.n / (XN / 2) : (p.n + XN - 1) / XN;
+    a.groups = p.groups;
+    a.rows = p.rows;
+    a.offsets = p.offsets;
+    a.a_scales = p.a_scales;
+    a.sb_tiles = b_rows / 128;
+    a.half = glu ? p.n : 0;
+    a.out = p.out;
+    a.out_codes = p.out_codes;
+    a.out_scales = p.out_scales;
+    a.status = p.status;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(2 * 74, 1, 1);
+    cfg.blockDim = dim3(kXThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    static int max_clusters[64] = {};
+    if (max_clusters[dev] == 0) {  // co-resident clusters (one CTA an SM at any group count)
+        cfg.numAttrs = 1;          // the cluster shape only
+        int n = 0;
+        err = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+        if (err != cudaSuccess) return err;
+        if (n <= 0) return cudaErrorInvalidConfiguration;
+        max_clusters[dev] = n;
+    }
+    // row tiles at most: one partial tile per group that has rows, and the full ones
+    const int64_t partial = p.rows < p.groups ? p.rows : p.groups;
+    int64_t clusters = (p.rows / XM + partial) * a.n_tiles;
+    if (clusters > max_clusters[dev]) clusters = max_clusters[dev];
+    cfg.gridDim = dim3((unsigned)(2 * clusters), 1, 1);
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, ma, mb, ms, mo, a);
+}
+
+}  // namespace
+
+cudaError_t launch_mx_gemm(const MxProblem& p, cudaStream_t st)
+{
+    if (p.k % 128 != 0 || p.n % 128 != 0) return cudaErrorInvalidValue;
+    if (!p.swiglu) return launch_mode<MX_BF16>(p, st);
+    return p.out_codes != nullptr ? launch_mode<MX_SWIGLU_QUANT>(p, st)
+                                  : launch_mode<MX_SWIGLU>(p, st);
+}
+
+}  // namespace moe

@@ -22,7 +22,8 @@ from . import _native as N
 SOFTMAX = N.MOE_SOFTMAX
 SIGMOID = N.MOE_SIGMOID
 SQRTSOFTPLUS = N.MOE_SQRTSOFTPLUS
-STATUS_NAMES = ("nan_tokens", "zero_denominator", "bad_expert_id", "pipeline_timeout")
+STATUS_NAMES = ("nan_tokens", "zero_denominator", "bad_expert_id", "pipeline_timeout",
+                "bad_rows")
 
 
 class MoeError(RuntimeError):
@@ -584,6 +585,159 @@ def forward_host(cfg: Config, x_host, w_router, w13, w2, logit_bias=None, sel_bi
     if check:
         check_status(st)
     return out_host
+
+
+# ------------------------------------------------------------------ experts in 4 bits
+
+def mx_quantize(x):
+    """Rows of x [R,K] (bf16, fp16 or fp32, K a multiple of 32) in the microscaled 4-bit format
+    (moe_mx_quantize): (codes [R,K/2], scales [R,K/32]), both uint8."""
+    _act(x, "x")
+    dev, (R, K) = x.device, x.shape
+    codes = torch.empty(R, K // 2, dtype=torch.uint8, device=dev)
+    scales = torch.empty(R, K // 32, dtype=torch.uint8, device=dev)
+    _rc(_call(dev, N.load().moe_mx_quantize, R, K, _DTYPES[x.dtype], 0, _p(x), _p(codes),
+              _p(scales)), "moe_mx_quantize")
+    return codes, scales
+
+
+def mx_weight(w):
+    """Expert weights [E,N,K] (or one matrix [N,K]; N and K multiples of 128) in the microscaled
+    4-bit format, as the products take them: (codes [E,N,K/2], scales in the tensor core's tiles
+    [E,N/128,K/128,512]), both uint8."""
+    if w.dim() not in (2, 3) or w.dtype not in _DTYPES or not w.is_contiguous():
+        raise MoeError(f"w: a contiguous [E,N,K] or [N,K] bf16, fp16 or fp32 tensor is expected, "
+                       f"got {w.dtype} {tuple(w.shape)}")
+    *lead, n, k = w.shape
+    if n % 128 or k % 128:
+        raise MoeError(f"w: N and K must be multiples of 128, got {n} and {k}")
+    dev = w.device
+    codes = torch.empty(*lead, n, k // 2, dtype=torch.uint8, device=dev)
+    scales = torch.empty(*lead, n // 128, k // 128, 512, dtype=torch.uint8, device=dev)
+    rows = w.numel() // k if k else 0
+    _rc(_call(dev, N.load().moe_mx_quantize, rows, k, _DTYPES[w.dtype], 1, _p(w), _p(codes),
+              _p(scales)), "moe_mx_quantize")
+    return codes, scales
+
+
+def mx_dequantize(codes, scales, dtype=torch.bfloat16):
+    """The values of mx_quantize's codes [R,K/2] and scales [R,K/32], rounded to dtype: [R,K]."""
+    dev = codes.device
+    if codes.dim() != 2 or dtype not in _DTYPES or codes.shape[1] % 16:
+        raise MoeError(f"codes {tuple(codes.shape)} to {dtype}: [R, K/2] with K a multiple of 32, "
+                       "and bf16, fp16 or fp32, are expected")
+    R, K = codes.shape[0], 2 * codes.shape[1]
+    _need(codes, "codes", torch.uint8, (R, K // 2), dev)
+    _need(scales, "scales", torch.uint8, (R, K // 32), dev)
+    out = torch.empty(R, K, dtype=dtype, device=dev)
+    _rc(_call(dev, N.load().moe_mx_dequantize, R, K, _DTYPES[dtype], _p(codes), _p(scales),
+              _p(out)), "moe_mx_dequantize")
+    return out
+
+
+def _mx_need(w, name, shape, dev):
+    """4-bit weights (codes, tiled scales) for matrices of this shape [..., N, K]."""
+    if w is None or len(w) != 2:
+        raise MoeError(f"{name}: (codes, scales) of mx_weight() are expected")
+    *lead, n, k = shape
+    _need(w[0], f"{name} codes", torch.uint8, (*lead, n, k // 2), dev)
+    _need(w[1], f"{name} scales", torch.uint8, (*lead, n // 128, k // 128, 512), dev)
+    return w
+
+
+def mx_grouped_gemm(codes, scales, offsets, w_codes, w_scales, swiglu: bool = False, out=None,
+                    status=None, check: bool = True):
+    """Rows in 4 bits (mx_quantize), grouped by offsets [E+1], times 4-bit weights (mx_weight of
+    [E,N,K]): [R,N] bf16, or with swiglu silu(first N/2 columns) * last N/2, [R,N/2]
+    (moe_mx_grouped_gemm). Rows outside every group are left as they were in out."""
+    dev = codes.device
+    if w_codes.dim() != 3 or codes.dim() != 2:
+        raise MoeError("codes [R, K/2] and w_codes [E, N, K/2] are expected")
+    R, K = codes.shape[0], 2 * codes.shape[1]
+    E, n = w_codes.shape[:2]
+    if n % (256 if swiglu else 128) or K % 128:
+        raise MoeError(f"N {n} and K {K}: multiples of {256 if swiglu else 128} and 128")
+    _need(codes, "codes", torch.uint8, (R, K // 2), dev)
+    _need(scales, "scales", torch.uint8, (R, K // 32), dev)
+    _need(offsets, "offsets", torch.int32, (E + 1,), dev)
+    _mx_need((w_codes, w_scales), "w", (E, n, K), dev)
+    shape = (R, n // 2 if swiglu else n)
+    out = torch.empty(shape, dtype=torch.bfloat16, device=dev) if out is None else out
+    _need(out, "out", torch.bfloat16, shape, dev)
+    st = new_status(dev) if status is None and check else status
+    _rc(_call(dev, N.load().moe_mx_grouped_gemm, R, K, n, E, int(bool(swiglu)), _p(codes),
+              _p(scales), _p(offsets), _p(w_codes), _p(w_scales), _p(out), _p(st)),
+        "moe_mx_grouped_gemm")
+    if check:
+        check_status(st)
+    return out
+
+
+def _mx_experts(cfg, w13, w2, w13_s, w2_s, dev):
+    H, E, I, Is = cfg.H, cfg.E, cfg.I, cfg.I_shared
+    _mx_need(w13, "w13", (E, 2 * I, H), dev)
+    _mx_need(w2, "w2", (E, H, I), dev)
+    if not Is:
+        return [*map(_p, (*w13, *w2))] + [None] * 4
+    _mx_need(w13_s, "w13_s", (2 * Is, H), dev)
+    _mx_need(w2_s, "w2_s", (H, Is), dev)
+    return [*map(_p, (*w13, *w2, *w13_s, *w2_s))]
+
+
+def mx_grouped_ffn(cfg: Config, x, dest_row, offsets, w13, w2, w13_s=None, w2_s=None, ws=None,
+                   status=None, check: bool = True):
+    """The expert boundary with 4-bit experts (moe_mx_grouped_ffn): w13, w2 (and the shared
+    expert's) as mx_weight() returned them, dest_row and offsets from permute(). Returns
+    (y [T*K,H], y_shared [T,H] or None)."""
+    dev = x.device
+    T, H, E, K, Is = cfg.T, cfg.H, cfg.E, cfg.K, cfg.I_shared
+    _need(x, "x", torch.bfloat16, (T, H), dev)
+    _need(dest_row, "dest_row", torch.int32, (T, K), dev)
+    _need(offsets, "offsets", torch.int32, (E + 1,), dev)
+    w = _mx_experts(cfg, w13, w2, w13_s, w2_s, dev)
+    y = torch.empty(T * K, H, dtype=torch.bfloat16, device=dev)
+    y_s = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if Is else None
+    nbytes = workspace_bytes(cfg, N.MOE_STAGE_MX_FFN)
+    ws = _ws(nbytes, dev, ws)
+    st = new_status(dev) if status is None and check else status
+    _rc(_call(dev, N.load().moe_mx_grouped_ffn, ctypes.byref(cfg.c()), _p(x), _p(dest_row),
+              _p(offsets), *w, _p(y), _p(y_s), _p(st), _p(ws), nbytes), "moe_mx_grouped_ffn")
+    if check:
+        check_status(st)
+    return y, y_s
+
+
+def mx_forward(cfg: Config, x, w_router, w13, w2, logit_bias=None, sel_bias=None, token_mask=None,
+               w13_s=None, w2_s=None, out=None, ws=None, status=None, keep: bool = False,
+               check: bool = True):
+    """The MoE layer with 4-bit experts in one call (moe_mx_forward): as forward(), with w13, w2
+    (and the shared expert's) as mx_weight() returned them; the router stays bf16."""
+    dev = x.device
+    T, H, E, K = cfg.T, cfg.H, cfg.E, cfg.K
+    _need(x, "x", torch.bfloat16, (T, H), dev)
+    _need(w_router, "w_router", torch.bfloat16, (E, H), dev)
+    w = _mx_experts(cfg, w13, w2, w13_s, w2_s, dev)
+    _opt(logit_bias, "logit_bias", torch.float32, (E,), dev)
+    _opt(sel_bias, "sel_bias", torch.float32, (E,), dev)
+    _opt(token_mask, "token_mask", torch.uint8, (T,), dev)
+    out = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if out is None else out
+    _need(out, "out", torch.bfloat16, (T, H), dev)
+    nbytes = workspace_bytes(cfg, N.MOE_STAGE_MX_FORWARD)
+    ws = _ws(nbytes, dev, ws)
+    st = new_status(dev) if status is None else status
+    b = {}
+    if keep:
+        b = {"logits": torch.empty(T, E, dtype=torch.float32, device=dev),
+             "topk_ids": torch.empty(T, K, dtype=torch.int32, device=dev),
+             "topk_w": torch.empty(T, K, dtype=torch.float32, device=dev),
+             "offsets": torch.empty(E + 1, dtype=torch.int32, device=dev)}
+    _rc(_call(dev, N.load().moe_mx_forward, ctypes.byref(cfg.c()), _p(x), _p(w_router),
+              _p(logit_bias), _p(sel_bias), _p(token_mask), *w, _p(out), _p(b.get("logits")),
+              _p(b.get("topk_ids")), _p(b.get("topk_w")), _p(b.get("offsets")), _p(st), _p(ws),
+              nbytes), "moe_mx_forward")
+    if check:
+        check_status(st)
+    return (out, b) if keep else out
 
 
 class MoELayer:

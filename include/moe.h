@@ -79,6 +79,7 @@ extern "C" {
 #define MOE_ST_ZERO_DENOM 1     /* tokens whose renormalisation denominator was 0 */
 #define MOE_ST_BAD_EXPERT_ID 2  /* expert ids >= E met by the dispatch (not counting -1) */
 #define MOE_ST_PIPE_TIMEOUT 3   /* a tensor-core pipeline wait gave up (result invalid) */
+#define MOE_ST_BAD_ROWS 4       /* row offsets or destination rows outside their buffers */
 #define MOE_STATUS_WORDS 8
 
 /* stages, for moe_workspace_bytes */
@@ -89,6 +90,8 @@ extern "C" {
 #define MOE_STAGE_FORWARD 4
 #define MOE_STAGE_STATS 5
 #define MOE_STAGE_BACKWARD 6
+#define MOE_STAGE_MX_FFN 7
+#define MOE_STAGE_MX_FORWARD 8
 
 /* number of CUDA events moe_forward can record (stage boundaries), see moe_forward */
 #define MOE_NUM_STAGE_EVENTS 8
@@ -480,6 +483,93 @@ MOE_API int moe_residual_norm_backward(const moe_norm_cfg* cfg, const void* r, c
 MOE_API int moe_dropout(int64_t T, int32_t H, int32_t dtype, double p, const void* x,
                         const int64_t* rng, int64_t first_row, const int32_t* row_ids, void* out,
                         void* stream);
+
+/* ------------------------------------------------------------ experts in 4 bits
+ *
+ * The microscaled 4-bit format (OCP Microscaling Formats v1.0, MXFP4) of a row of K values:
+ * e2m1 codes (0, 1/2, 1, 3/2, 2, 3, 4, 6 and their negatives), two to a byte, the even column
+ * in the low nibble, and one e8m0 scale byte s = 127 + e per 32 columns, for 2^e. Quantisation:
+ *   e = max(-127, floor(log2(amax of the block)) - 2),  code = e2m1(x 2^-e)
+ * to nearest even, saturated at +-6. A block with an infinity or a NaN gets the scale 255 (NaN)
+ * and codes 0, and every result that meets it is NaN.
+ *
+ * Weights keep their scales in the tensor core's tiles: for a matrix of N rows and K columns
+ * (both multiples of 128) tile (N / 128, K / 128) is 512 bytes, the scale of row r and block b
+ * of the tile at 16 (r % 32) + 4 (r / 32) + b.
+ */
+
+/*
+ * x [rows, K] of `dtype` -> codes [rows, K / 2], scales [rows, K / 32], or with tiled = 1 the
+ * scales in tiles, [rows / 128, K / 128, 512] (a batch of matrices of N rows each, N a multiple
+ * of 128, is one call with rows = batch * N). K % 32 == 0, tiled: rows and K % 128 == 0;
+ * 0 <= rows, rows * K < 2^42, K <= 2^20.
+ */
+MOE_API int moe_mx_quantize(int64_t rows, int32_t K, int32_t dtype, int32_t tiled, const void* x,
+                            uint8_t* codes, uint8_t* scales, void* stream);
+
+/* The values that codes and row-major scales stand for, rounded to `dtype`. */
+MOE_API int moe_mx_dequantize(int64_t rows, int32_t K, int32_t dtype, const uint8_t* codes,
+                              const uint8_t* scales, void* out, void* stream);
+
+/*
+ * Grouped product of 4-bit rows and 4-bit weights, fp32 accumulation on the tensor cores:
+ * for every row r of group g (offsets[g] <= r < offsets[g + 1])
+ *   v[c] = A_r . B_g[c],  out_r = bf16(v)                                (swiglu = 0)
+ *   out_r[c] = bf16( silu(v[c]) * v[N / 2 + c] ), c < N / 2              (swiglu = 1)
+ * A row's result depends on that row and the weights alone, with K in a fixed order. Rows
+ * outside every group are left as they were.
+ *
+ *  a_codes [rows, K / 2], a_scales [rows, K / 32]  (from moe_mx_quantize).
+ *  offsets  [groups + 1] int32 device, or NULL (groups = 1: all rows). An offset outside
+ *           [0, rows] or below its predecessor counts in status[MOE_ST_BAD_ROWS] and is clamped.
+ *  b_codes  [groups, N, K / 2], b_scales [groups, N / 128, K / 128, 512].
+ *  out      [rows, N] bf16, or [rows, N / 2] with swiglu.
+ *  status   int32[MOE_STATUS_WORDS] device, cleared first; may be NULL.
+ * 0 <= rows < 2^31, 1 <= groups <= 1024, N and K multiples of 128 from 128 to 32768 (swiglu:
+ * N a multiple of 256, up to 65536).
+ */
+MOE_API int moe_mx_grouped_gemm(int64_t rows, int32_t K, int32_t N, int32_t groups,
+                                int32_t swiglu, const uint8_t* a_codes, const uint8_t* a_scales,
+                                const int32_t* offsets, const uint8_t* b_codes,
+                                const uint8_t* b_scales, uint16_t* out, int32_t* status,
+                                void* stream);
+
+/*
+ * The expert boundary with 4-bit experts, the counterpart of moe_grouped_ffn: every token is
+ * quantised once and its codes are dispatched, h is quantised in the epilogue of gate_up.
+ *   q = mx(x_t),  h_r = bf16( silu(q . W13[e, 0:I]^T) * (q . W13[e, I:2I]^T) ),
+ *   y_r = bf16( mx(h_r) . W2[e]^T )
+ * The bits of moe_mx_quantize, two moe_mx_grouped_gemm and the quantisation of h between them.
+ *
+ *  x        [T,H] bf16; dest_row [T,K] and offsets [E+1] from moe_permute (x_perm is not
+ *           needed). Destinations at or past T*K count in MOE_ST_BAD_ROWS.
+ *  w13_codes [E, 2I, H/2], w2_codes [E, H, I/2] and their tiled scales; the shared expert's
+ *           ([2 I_shared, H/2], [H, I_shared/2]) when I_shared > 0.
+ *  y [T*K,H] bf16 out; y_shared [T,H] bf16 out with a shared expert.
+ *  ws moe_workspace_bytes(cfg, MOE_STAGE_MX_FFN) bytes.
+ */
+MOE_API int moe_mx_grouped_ffn(const moe_cfg* cfg, const uint16_t* x, const int32_t* dest_row,
+                               const int32_t* offsets, const uint8_t* w13_codes,
+                               const uint8_t* w13_scales, const uint8_t* w2_codes,
+                               const uint8_t* w2_scales, const uint8_t* w13_s_codes,
+                               const uint8_t* w13_s_scales, const uint8_t* w2_s_codes,
+                               const uint8_t* w2_s_scales, uint16_t* y, uint16_t* y_shared,
+                               int32_t* status, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The whole layer with 4-bit experts: moe_route -> moe_permute -> moe_mx_grouped_ffn ->
+ * moe_combine on one stream (router in bf16, as moe_forward). Arguments as there;
+ * ws moe_workspace_bytes(cfg, MOE_STAGE_MX_FORWARD) bytes.
+ */
+MOE_API int moe_mx_forward(const moe_cfg* cfg, const uint16_t* x, const uint16_t* w_router,
+                           const float* logit_bias, const float* sel_bias,
+                           const uint8_t* token_mask, const uint8_t* w13_codes,
+                           const uint8_t* w13_scales, const uint8_t* w2_codes,
+                           const uint8_t* w2_scales, const uint8_t* w13_s_codes,
+                           const uint8_t* w13_s_scales, const uint8_t* w2_s_codes,
+                           const uint8_t* w2_s_scales, uint16_t* out, float* logits,
+                           int32_t* topk_ids, float* topk_w, int32_t* offsets, int32_t* status,
+                           void* ws, size_t ws_bytes, void* stream);
 
 /* Text of a return code. */
 MOE_API const char* moe_status_string(int code);
