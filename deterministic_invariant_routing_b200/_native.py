@@ -97,7 +97,7 @@ SIGNATURES = {
     "moe_dropout": (_I, [_I64, ctypes.c_int32, ctypes.c_int32, ctypes.c_double, _P, _P, _I64, _P,
                          _P, _P]),
     "moe_mx_quantize": (_I, [_I64] + [ctypes.c_int32] * 3 + [_P] * 4),
-    "moe_mx_dequantize": (_I, [_I64] + [ctypes.c_int32] * 2 + [_P] * 4),
+    "moe_mx_dequantize": (_I, [_I64] + [ctypes.c_int32] * 3 + [_P] * 4),
     "moe_mx_grouped_gemm": (_I, [_I64] + [ctypes.c_int32] * 4 + [_P] * 8),
     "moe_mx_grouped_ffn": (_I, [_CFG] + [_P] * 15 + [_SZ, _P]),
     "moe_mx_forward": (_I, [_CFG] + [_P] * 20 + [_SZ, _P]),

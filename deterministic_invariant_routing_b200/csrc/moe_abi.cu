@@ -464,13 +464,14 @@ MxFfnLayout mx_ffn_layout(const moe_cfg& c)
         return o;
     };
     L.xq = take(A * c.H / 2);
-    L.xs = take(A * c.H / 32);
+    const size_t Ap = (A + 127) / 128 * 128, Tp = (T + 127) / 128 * 128;  // rows of scale tiles
+    L.xs = take(Ap * c.H / 32);
     L.hq = take(A * c.I / 2);
-    L.hs = take(A * c.I / 32);
+    L.hs = take(Ap * c.I / 32);
     L.tq = take(T * c.H / 2);
-    L.ts = take(T * c.H / 32);
+    L.ts = take(Tp * c.H / 32);
     L.sq = take(T * c.I_shared / 2);
-    L.ss = take(T * c.I_shared / 32);
+    L.ss = take(Tp * c.I_shared / 32);
     L.total = off;
     return L;
 }
@@ -1375,19 +1376,20 @@ MOE_API int moe_mx_quantize(int64_t rows, int32_t K, int32_t dtype, int32_t tile
         return MOE_ERR_SHAPE;
     if (dtype != MOE_BF16 && dtype != MOE_F16 && dtype != MOE_F32) return MOE_ERR_SHAPE;
     if (tiled != 0 && tiled != 1) return MOE_ERR_ARG;
-    if (tiled && (rows % 128 != 0 || K % 128 != 0)) return MOE_ERR_SHAPE;
     if (rows == 0) return MOE_OK;
     if (x == nullptr || codes == nullptr || scales == nullptr) return MOE_ERR_ARG;
     int rc;
-    if ((rc = check_aligned({x, codes})) != MOE_OK) return rc;
+    if ((rc = check_aligned({x, codes, tiled ? scales : nullptr})) != MOE_OK) return rc;
     if ((rc = check_device()) != MOE_OK) return rc;
     return cuda_rc(launch_mx_quantize(rows, K, dtype, tiled != 0, x, codes, scales,
                                       static_cast<cudaStream_t>(stream)));
 }
 
-MOE_API int moe_mx_dequantize(int64_t rows, int32_t K, int32_t dtype, const uint8_t* codes,
-                              const uint8_t* scales, void* out, void* stream)
+MOE_API int moe_mx_dequantize(int64_t rows, int32_t K, int32_t dtype, int32_t tiled,
+                              const uint8_t* codes, const uint8_t* scales, void* out,
+                              void* stream)
 {
+    if (tiled != 0 && tiled != 1) return MOE_ERR_ARG;
     if (rows < 0 || K < 32 || K > (1 << 20) || K % 32 != 0 || rows >= ((int64_t)1 << 42) / K)
         return MOE_ERR_SHAPE;
     if (dtype != MOE_BF16 && dtype != MOE_F16 && dtype != MOE_F32) return MOE_ERR_SHAPE;
@@ -1396,7 +1398,7 @@ MOE_API int moe_mx_dequantize(int64_t rows, int32_t K, int32_t dtype, const uint
     int rc;
     if ((rc = check_aligned({codes, out})) != MOE_OK) return rc;
     if ((rc = check_device()) != MOE_OK) return rc;
-    return cuda_rc(launch_mx_dequantize(rows, K, dtype, codes, scales, out,
+    return cuda_rc(launch_mx_dequantize(rows, K, dtype, tiled != 0, codes, scales, out,
                                         static_cast<cudaStream_t>(stream)));
 }
 

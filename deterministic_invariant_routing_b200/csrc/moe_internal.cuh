@@ -135,13 +135,14 @@ cudaError_t launch_mx_quantize(int64_t rows, int32_t K, int dtype, bool tiled, c
 cudaError_t launch_mx_scatter(const moe_cfg& c, const uint16_t* x, const int32_t* dest_row,
                               uint8_t* codes, uint8_t* scales, uint8_t* tok_codes,
                               uint8_t* tok_scales, int32_t* status, cudaStream_t st);
-cudaError_t launch_mx_dequantize(int64_t rows, int32_t K, int dtype, const uint8_t* codes,
-                                 const uint8_t* scales, void* out, cudaStream_t st);
+cudaError_t launch_mx_dequantize(int64_t rows, int32_t K, int dtype, bool tiled,
+                                 const uint8_t* codes, const uint8_t* scales, void* out,
+                                 cudaStream_t st);
 
 // grouped product of 4-bit rows and 4-bit weights (mx_gemm.cu)
 struct MxProblem {
     const uint8_t* a;          // [rows, k / 2] codes
-    const uint8_t* a_scales;   // [rows, k / 32]
+    const uint8_t* a_scales;   // its scales in 128-row tiles
     int64_t rows;              // < 2^31
     const int32_t* offsets;    // device [groups + 1], or NULL: one group of all rows
     int groups;
@@ -151,7 +152,7 @@ struct MxProblem {
     bool swiglu;
     uint16_t* out;             // [rows, n] bf16, or with out_codes:
     uint8_t* out_codes;        // [rows, n / 2] and
-    uint8_t* out_scales;       // [rows, n / 32], quantised from the bf16 values (swiglu only)
+    uint8_t* out_scales;       // scales in tiles, quantised from the bf16 values (swiglu only)
     int32_t* status;
 };
 cudaError_t launch_mx_gemm(const MxProblem& p, cudaStream_t st);

@@ -73,7 +73,7 @@ __device__ __forceinline__ uint32_t mx_encode8(const float (&v)[8], uint32_t s)
 // Offset of the scale of (row, block) in the tensor core's tiles: 128 rows by 4 blocks of 32
 // (128 columns) are 512 consecutive bytes, row r at 16 (r % 32) + 4 (r / 32), its 4 blocks in
 // order; tiles follow along the row first. `row` counts over all matrices of a batch (each a
-// multiple of 128 rows).
+// multiple of 128 rows); `blocks` is the blocks of a row, rounded up to 4.
 __host__ __device__ __forceinline__ int64_t mx_tiled_scale(int64_t row, int block, int blocks)
 {
     const int r = (int)(row & 127);

@@ -10,18 +10,22 @@
 // for the 512 cycles its four instructions need.
 //
 // Scales: an instruction reads them from TMEM, 4 bytes (4 blocks of 32) per row in a 32-bit
-// column for every 32 rows. They are staged beside the operands and copied in by tcgen05.cp
-// (32x128b.warpx4: 512 bytes of shared memory, 128 rows by 4 blocks, to 4 columns), issued in
-// order before the instructions that read them:
-//   B: stored in exactly those tiles (the layout weights are kept in), loaded by TMA; each CTA
-//      needs the scales of all 256 columns.
-//   A: rows start anywhere (an expert's first row is not a multiple of 128), so a warp reads
-//      them from the row-major array, four rows a lane -- the lane's 16 bytes of a tile -- a few
-//      k-blocks ahead, and writes them to shared memory itself.
+// column for every 32 rows. Both operands keep them in tiles of 128 rows by 4 blocks (512 bytes,
+// mx_tiled_scale), which TMA brings in beside the operands and tcgen05.cp (32x128b.warpx4) copies
+// to 4 columns, issued in order before the instructions that read them. Each CTA needs the
+// scales of its 128 rows and of all 256 columns. A tile of rows therefore starts on a multiple of
+// 128 of the row index: an expert's first tile may begin with rows of the expert before it,
+// which are computed and not stored. (Rows started at the expert's first row, with a warp
+// reading row-major scales four k-blocks ahead and writing the tile itself, measured 2060
+// cycles a k-block against 512: the fence between its writes and the copy waits for its reads.)
+//
+// TMEM: two accumulators of 256 columns and 24 columns of scales do not fit in 512, so the
+// accumulators share 32 columns ([0, 256) and [224, 480)): a tile's epilogue reads those first
+// and lets the next tile's instructions start after them.
 //
 // Arithmetic per row: k-blocks in increasing order, four K = 64 steps each (two in a last block
 // of 128 columns), one accumulator; nothing depends on where the row sits, on its expert's
-// other rows or on T. Rows past the group's end are computed and never stored.
+// other rows or on T. Rows outside the group are computed and never stored.
 //
 // Every wait is bounded (MOE_ST_PIPE_TIMEOUT); offsets outside [0, rows] are clamped and counted
 // in MOE_ST_BAD_ROWS, so no tile reaches past the buffers.
@@ -41,14 +45,15 @@ constexpr uint32_t kXSA = 1024;         // scales of 128 rows, two tiles of 4 bl
 constexpr uint32_t kXSB = 2048;         // scales of 256 columns
 constexpr uint32_t kXStage = kXA + kXB + kXSA + kXSB;
 constexpr int kXS = 5;                  // stages
+constexpr uint32_t kXBox = 32 * XK / 2; // a 32-row box of A
 constexpr int kXEpiWarps = 8;
 constexpr uint32_t kXEpi = kXEpiWarps * 2 * 2048;
-constexpr int kXThreads = 32 * (2 + kXEpiWarps + 1);
-constexpr int kXBars = 2 * kXS + 3;
-constexpr uint32_t kXCols = 512;        // TMEM columns: the accumulator, then the scales
-constexpr uint32_t kXTmemSA = 256, kXTmemSB = 264;
+constexpr int kXThreads = 32 * (2 + kXEpiWarps);
+constexpr int kXBars = 2 * kXS + 6;
+constexpr uint32_t kXCols = 512;        // TMEM columns
+constexpr uint32_t kXAcc1 = 224;        // the second accumulator; the first is at 0
+constexpr uint32_t kXTmemSA = 480, kXTmemSB = 488;
 constexpr uint16_t kXPair = 0x3;
-constexpr int kXAhead = 4;              // k-blocks the A scales are read ahead
 
 enum MxEpilogue { MX_BF16 = 0, MX_SWIGLU = 1, MX_SWIGLU_QUANT = 2 };
 
@@ -56,19 +61,36 @@ struct MxArgs {
     int k, k_blocks, n, n_tiles, groups;
     int64_t rows;
     const int32_t* offsets;  // [groups + 1], or NULL: one group of all rows
-    const uint8_t* a_scales; // [rows, k / 32]
     int sb_tiles;            // 128-row scale tiles per group of B
     int half;                // SwiGLU: n, the first up row; 0 otherwise
     uint16_t* out;           // [rows, n] bf16
-    uint8_t* out_codes;      // MX_SWIGLU_QUANT: [rows, n / 2] and [rows, n / 32]
+    uint8_t* out_codes;      // MX_SWIGLU_QUANT: [rows, n / 2], and scales in tiles
     uint8_t* out_scales;
     int32_t* status;
 };
 
 struct MxTile {
     int g, n;
-    int64_t row0, row_end;
+    int64_t row0, row_beg, row_end;  // the tile's first row, the group's rows
 };
+
+// rows of a group that starts at `beg`, tiled from the multiple of 128 below it
+__device__ __forceinline__ int mx_row_tiles(int beg, int end)
+{
+    return end > beg ? (end - (beg & ~127) + XM - 1) / XM : 0;
+}
+
+// which of CTA `rank`'s four 32-row boxes hold rows of the group
+__device__ __forceinline__ uint32_t mx_boxes(const MxTile& t, uint32_t rank)
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t r = t.row0 + (int64_t)rank * XH + 32 * j;
+        if (r < t.row_end && r + 32 > t.row_beg) m |= 1u << j;
+    }
+    return m;
+}
 
 // kind::mxf4 with e2m1 operands (format 1), e8m0 scales (bit 23), M = 256, N = 256, both K-major;
 // the scale bytes of a 32-bit column that the instruction reads start at byte `id` (0 or 2)
@@ -105,7 +127,10 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t saddr)
 
 template <int MODE>
 __global__ void __launch_bounds__(kXThreads, 1)
-    mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+    mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
+                   const __grid_constant__ CUtensorMap tmA32,
+                   const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ CUtensorMap tmSA,
                    const __grid_constant__ CUtensorMap tmSB,
                    const __grid_constant__ CUtensorMap tmO, MxArgs args)
 {
@@ -122,8 +147,10 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const uint32_t bar0 = smem_u32(bars);
     auto full_bar = [&](int s) { return bar0 + 8u * (uint32_t)s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (uint32_t)(kXS + s); };
-    const uint32_t tfull = bar0 + 8u * (uint32_t)(2 * kXS);
-    const uint32_t tempty = tfull + 8u, drain = tfull + 16u;
+    auto tfull_bar = [&](int a) { return bar0 + 8u * (uint32_t)(2 * kXS + a); };
+    auto tempty_bar = [&](int a) { return bar0 + 8u * (uint32_t)(2 * kXS + 2 + a); };
+    const uint32_t tover = bar0 + 8u * (uint32_t)(2 * kXS + 4);  // the shared columns are read
+    const uint32_t drain = tover + 8u;
     uint32_t* misc = reinterpret_cast<uint32_t*>(bars + kXBars);  // [0] tmem, [1] abort
     volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
     int32_t* prefix = reinterpret_cast<int32_t*>(misc + 4);  // [groups + 1] row tiles before g
@@ -137,11 +164,14 @@ __global__ void __launch_bounds__(kXThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kXS; ++s) {
-            mbar_init(full_bar(s), 3);  // the leader's byte count, each CTA's A scales
+            mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
         }
-        mbar_init(tfull, 1);
-        mbar_init(tempty, 2 * kXEpiWarps * 32);
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(tfull_bar(a), 1);
+            mbar_init(tempty_bar(a), 2 * kXEpiWarps * 32);
+        }
+        mbar_init(tover, kXEpiWarps * 32);  // half of each CTA's epilogue warps
         mbar_init(drain, 1);
         misc[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -157,9 +187,9 @@ __global__ void __launch_bounds__(kXThreads, 1)
             if (o < 0 || o > args.rows) bad = true;
             return o < 0 ? 0 : (o > args.rows ? (int)args.rows : o);
         };
-        auto tiles_of = [&](int n) -> int {
-            if (n < 0) bad = true;
-            return n > 0 ? (n + XM - 1) / XM : 0;
+        auto tiles_of = [&](int beg, int end) -> int {
+            if (end < beg) bad = true;
+            return mx_row_tiles(beg, end);
         };
         const int per = (G + 31) / 32;
         const int beg = lane * per < G ? lane * per : G;
@@ -168,7 +198,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         for (int g = beg; g < end; ++g) {
             const int r0 = row_off(g);
             offs[g] = r0;
-            sum += tiles_of(row_off(g + 1) - r0);
+            sum += tiles_of(r0, row_off(g + 1));
         }
         if (lane == 0) offs[G] = row_off(G);
         int incl = sum;
@@ -180,7 +210,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         int run = incl - sum;
         for (int g = beg; g < end; ++g) {
             prefix[g] = run;
-            run += tiles_of(row_off(g + 1) - row_off(g));
+            run += tiles_of(row_off(g), row_off(g + 1));
         }
         if (lane == 31) prefix[G] = incl;
         if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0)
@@ -202,7 +232,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
             else hi = mid - 1;
         }
         ti.g = lo;
-        ti.row0 = (int64_t)offs[lo] + (int64_t)(mt - prefix[lo]) * XM;
+        ti.row_beg = offs[lo];
+        ti.row0 = (ti.row_beg & ~(int64_t)127) + (int64_t)(mt - prefix[lo]) * XM;
         ti.row_end = offs[lo + 1];
         return ti;
     };
@@ -220,6 +251,12 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 const int b0 = ti.g * args.sb_tiles + (kGlu ? ti.n : 2 * ti.n);  // 128-row tiles
                 const int b1 = kGlu ? b0 + args.half / 128 : b0 + 1;
                 const int brow = (leader ? b0 : b1) * 128;
+                // a whole tile's rows come in one box; of a partial one only the 32-row boxes
+                // with rows of the group (decode-sized groups read few rows)
+                const uint32_t mine = mx_boxes(ti, rank), other = mx_boxes(ti, rank ^ 1u);
+                const uint32_t bytes = 2 * (kXB + kXSA + kXSB) +
+                                       kXBox * (uint32_t)(__popc(mine) + __popc(other));
+                const int sa = (int)(ti.row0 / 128 + rank) * kc;
                 bool ok = true;
                 for (int kb = 0; kb < args.k_blocks; ++kb) {
                     if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.status)) {
@@ -227,9 +264,18 @@ __global__ void __launch_bounds__(kXThreads, 1)
                         break;
                     }
                     const uint32_t fb = fb0 + 8u * (uint32_t)stage;
-                    if (leader) mbar_expect_tx(full_bar(stage), 2 * (kXA + kXB + kXSB));
+                    if (leader) mbar_expect_tx(full_bar(stage), bytes);
                     const uint32_t ss = (uint32_t)stage;
-                    tma_load_2d_pair(sA0 + ss * kXA, &tmA, kb * (XK / 2), arow, fb);
+                    if (mine == 15u) {
+                        tma_load_2d_pair(sA0 + ss * kXA, &tmA, kb * (XK / 2), arow, fb);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (mine >> j & 1u)
+                                tma_load_2d_pair(sA0 + ss * kXA + j * kXBox, &tmA32, kb * (XK / 2),
+                                                 arow + 32 * j, fb);
+                    }
+                    tma_load_2d_pair(sSA0 + ss * kXSA, &tmSA, 0, sa + 2 * kb, fb);
                     tma_load_2d_pair(sB0 + ss * kXB, &tmB, kb * (XK / 2), brow, fb);
                     tma_load_2d_pair(sSB0 + ss * kXSB, &tmSB, 0, b0 * kc + 2 * kb, fb);
                     tma_load_2d_pair(sSB0 + ss * kXSB + 1024u, &tmSB, 0, b1 * kc + 2 * kb, fb);
@@ -260,8 +306,14 @@ __global__ void __launch_bounds__(kXThreads, 1)
             uint32_t phase = 0;
             int i = 0;
             for (int t = cluster; t < total && !*abort_flag; t += nclusters, ++i) {
-                if (!wait_bounded(tempty, ((uint32_t)i & 1u) ^ 1u, abort_flag, args.status)) break;
+                const int acc = i & 1;
+                if (!wait_bounded(tempty_bar(acc), (((uint32_t)i >> 1) & 1u) ^ 1u, abort_flag,
+                                  args.status))
+                    break;
+                if (i > 0 && !wait_bounded(tover, ((uint32_t)i - 1u) & 1u, abort_flag, args.status))
+                    break;
                 tc_fence_after();
+                const uint32_t d = tmem_base + (acc ? kXAcc1 : 0u);
                 bool ok = true;
                 for (int kb = 0; kb < args.k_blocks; ++kb) {
                     if (!wait_bounded(full_bar(stage), phase, abort_flag, args.status)) {
@@ -283,7 +335,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const uint64_t step = (uint64_t)(2 * (2 * c + h));
-                            mma_mxf4_pair(tmem_base, ad + step, bd + step,
+                            mma_mxf4_pair(d, ad + step, bd + step,
                                           h ? mx_idesc(XM, XN, 2) : mx_idesc(XM, XN, 0),
                                           tsa + 4u * c, tsb + 8u * c,
                                           (kb | c | h) != 0 ? 1u : 0u);
@@ -296,99 +348,19 @@ __global__ void __launch_bounds__(kXThreads, 1)
                     }
                 }
                 if (!ok) break;
-                mma_commit_pair_mc(tfull, kXPair);
+                mma_commit_pair_mc(tfull_bar(acc), kXPair);
             }
             mma_commit_pair(drain);
             wait_bounded(drain, 0u, abort_flag, args.status, false);
-        }
-    } else if (warp == 2 + kXEpiWarps) {
-        // -------------------------------------------------------------- A scales
-        // lane l holds rows l, l + 32, l + 64, l + 96 of this CTA's 128: bytes 16 l .. of a tile
-        const int blocks = args.k / 32;
-        const bool wide = args.k % 256 == 0;  // a row's 8 scales of a k-block are 8-byte aligned
-        const uint32_t fb0 = mapa_shared(full_bar(0), 0);
-        int it = cluster, ikb = 0;  // the k-block to read next
-        const uint8_t* src[4] = {nullptr, nullptr, nullptr, nullptr};
-        auto rows_of = [&](int t) {
-            if (t >= total) return;
-            const MxTile ti = decode(t);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t r = ti.row0 + (int64_t)rank * XH + 32 * j + lane;
-                src[j] = r < ti.row_end ? args.a_scales + r * blocks : nullptr;
-            }
-        };
-        auto read = [&](uint2 (&b)[4]) {
-            if (it >= total) return;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                b[j] = make_uint2(0u, 0u);
-                if (src[j] != nullptr) {
-                    const uint8_t* p = src[j] + ikb * 8;
-                    if (wide) {
-                        b[j] = *reinterpret_cast<const uint2*>(p);
-                    } else {
-                        b[j].x = *reinterpret_cast<const uint32_t*>(p);
-                        if (ikb * 8 + 4 < blocks) b[j].y = *reinterpret_cast<const uint32_t*>(p + 4);
-                    }
-                }
-            }
-            if (++ikb == args.k_blocks) {
-                ikb = 0;
-                it += nclusters;
-                rows_of(it);
-            }
-        };
-        uint2 buf[kXAhead][4];
-        rows_of(it);
-#pragma unroll
-        for (int d = 0; d < kXAhead; ++d) read(buf[d]);
-        int t = cluster, kb = 0, stage = 0;
-        uint32_t phase = 0;
-        bool run = t < total;
-        while (run) {
-#pragma unroll
-            for (int d = 0; d < kXAhead; ++d) {
-                if (run) {
-                    int ok = 1;
-                    if (lane == 0)
-                        ok = wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.status);
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
-                    if (!ok) {
-                        run = false;
-                    } else {
-                        const uint32_t dst = sSA0 + (uint32_t)stage * kXSA + (uint32_t)lane * 16u;
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst),
-                                     "r"(buf[d][0].x), "r"(buf[d][1].x), "r"(buf[d][2].x),
-                                     "r"(buf[d][3].x)
-                                     : "memory");
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 512u),
-                                     "r"(buf[d][0].y), "r"(buf[d][1].y), "r"(buf[d][2].y),
-                                     "r"(buf[d][3].y)
-                                     : "memory");
-                        fence_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(fb0 + 8u * (uint32_t)stage);
-                        read(buf[d]);
-                        if (++stage == kXS) {
-                            stage = 0;
-                            phase ^= 1u;
-                        }
-                        if (++kb == args.k_blocks) {
-                            kb = 0;
-                            t += nclusters;
-                            run = t < total;
-                        }
-                    }
-                }
-            }
         }
     } else {
         // -------------------------------------------------------------- epilogue
         const int q = warp & 3;  // TMEM lanes 32 q .. 32 q + 31
         const int row = q * 32 + lane;
-        const int c0 = 32 * ((warp - 2) >> 2);  // this warp's first 32-column chunk, then + 64
-        const uint32_t tempty_leader = mapa_shared(tempty, 0);
+        const int half = (warp - 2) >> 2;  // two warps a lane quarter: the first and last chunks
+        const uint32_t tempty_leader0 = mapa_shared(tempty_bar(0), 0);
+        const uint32_t tempty_leader1 = mapa_shared(tempty_bar(1), 0);
+        const uint32_t tover_leader = mapa_shared(tover, 0);
         const uint32_t ebuf = sE0 + (uint32_t)(warp - 2) * 4096u;
         uint32_t eb = 0;
         const uint32_t erow = (uint32_t)lane * 64u, eswz = ((uint32_t)lane >> 1) & 3u;
@@ -423,21 +395,32 @@ __global__ void __launch_bounds__(kXThreads, 1)
         for (int t = cluster; t < total && !*abort_flag; t += nclusters, ++i) {
             const MxTile ti = decode(t);
             int ok = 1;
-            if (lane == 0) ok = wait_bounded(tfull, (uint32_t)i & 1u, abort_flag, args.status);
+            const int acc = i & 1;
+            if (lane == 0)
+                ok = wait_bounded(tfull_bar(acc), ((uint32_t)i >> 1) & 1u, abort_flag, args.status);
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16);
+            const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (acc ? kXAcc1 : 0u);
+            // the shared columns are the first accumulator's last chunk and the second's first:
+            // each half starts at its outer end, and the half that meets them says so
+            const bool over = half == (acc ? 0 : 1);
+            auto release_shared = [&]() {
+                tc_fence_before();
+                mbar_arrive_cluster(tover_leader);
+            };
             const int64_t grow = ti.row0 + (int64_t)rank * XH + row;
-            const bool valid = grow < ti.row_end;
+            const bool valid = grow >= ti.row_beg && grow < ti.row_end;
             const int row_blk = (int)(ti.row0 + (int64_t)rank * XH + q * 32);
-            const bool full_blk = (int64_t)row_blk + 31 < ti.row_end;
+            const bool full_blk = row_blk >= ti.row_beg && (int64_t)row_blk + 31 < ti.row_end;
             if (kGlu) {
 #pragma unroll 1
-                for (int c = c0; c < XN / 2; c += 64) {
+                for (int k = 0; k < 2; ++k) {
+                    const int c = half ? 96 - 32 * k : 32 * k;
                     uint32_t g[32], u[32];
                     tmem_ld32(tbase + (uint32_t)c, g);
                     tmem_ld32(tbase + (uint32_t)(XN / 2 + c), u);
+                    if (k == 0 && over) release_shared();
                     uint32_t pk[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
@@ -473,16 +456,18 @@ __global__ void __launch_bounds__(kXThreads, 1)
                         }
                         *reinterpret_cast<uint4*>(args.out_codes + grow * (args.n / 2) + col / 2) =
                             make_uint4(code[0], code[1], code[2], code[3]);
-                        args.out_scales[grow * (args.n / 32) + col / 32] = (uint8_t)s;
+                        args.out_scales[mx_tiled_scale(grow, col / 32, args.n / 32)] = (uint8_t)s;
                     }
                 }
             } else {
 #pragma unroll 1
-                for (int c = c0; c < XN; c += 64) {
+                for (int k = 0; k < 4; ++k) {
+                    const int c = half ? 224 - 32 * k : 32 * k;
                     const int col = ti.n * XN + c;
-                    if (col >= args.n) break;  // past the last column (n a multiple of 128)
                     uint32_t r[32];
                     tmem_ld32(tbase + (uint32_t)c, r);
+                    if (k == 0 && over) release_shared();
+                    if (col >= args.n) continue;  // past the last column (n a multiple of 128)
                     uint32_t pk[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
@@ -491,7 +476,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 }
             }
             tc_fence_before();
-            mbar_arrive_cluster(tempty_leader);
+            mbar_arrive_cluster(acc ? tempty_leader1 : tempty_leader0);
         }
         if (lane == 0) bulk_wait_all();
     }
@@ -554,8 +539,11 @@ cudaError_t launch_mode(const MxProblem& p, cudaStream_t st)
     }
     const bool glu = MODE != MX_BF16;
     const int b_rows = glu ? 2 * p.n : p.n;
-    CUtensorMap ma, mb, ms, mo;
+    CUtensorMap ma, ma32, mb, msa, ms, mo;
     if (!make_codes_map(&ma, p.a, p.rows, p.k, XH)) return cudaErrorInvalidValue;
+    if (!make_codes_map(&ma32, p.a, p.rows, p.k, 32)) return cudaErrorInvalidValue;
+    if (!make_scale_map(&msa, p.a_scales, (p.rows + 127) / 128 * (p.k / 128)))
+        return cudaErrorInvalidValue;
     if (!make_codes_map(&mb, p.b, (int64_t)p.groups * b_rows, p.k, XH)) return cudaErrorInvalidValue;
     if (!make_scale_map(&ms, p.b_scales, (int64_t)p.groups * (b_rows / 128) * (p.k / 128)))
         return cudaErrorInvalidValue;
@@ -569,7 +557,6 @@ cudaError_t launch_mode(const MxProblem& p, cudaStream_t st)
     a.groups = p.groups;
     a.rows = p.rows;
     a.offsets = p.offsets;
-    a.a_scales = p.a_scales;
     a.sb_tiles = b_rows / 128;
     a.half = glu ? p.n : 0;
     a.out = p.out;
@@ -598,13 +585,13 @@ cudaError_t launch_mode(const MxProblem& p, cudaStream_t st)
         if (n <= 0) return cudaErrorInvalidConfiguration;
         max_clusters[dev] = n;
     }
-    // row tiles at most: one partial tile per group that has rows, and the full ones
+    // row tiles at most: two partial tiles per group that has rows, and the full ones
     const int64_t partial = p.rows < p.groups ? p.rows : p.groups;
-    int64_t clusters = (p.rows / XM + partial) * a.n_tiles;
+    int64_t clusters = (p.rows / XM + 2 * partial) * a.n_tiles;
     if (clusters > max_clusters[dev]) clusters = max_clusters[dev];
     cfg.gridDim = dim3((unsigned)(2 * clusters), 1, 1);
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, ma, mb, ms, mo, a);
+    return cudaLaunchKernelEx(&cfg, kernel, ma, ma32, mb, msa, ms, mo, a);
 }
 
 }  // namespace

@@ -16,11 +16,20 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t m)
     return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
 }
 
-// x [rows, 8 nvec], rows densely packed, as one run of vectors (a block never spans two rows)
-template <int DT, bool TILED>
+// Scales in tiles: lane 0 of the 16 that share 128 columns stores the word of their 4 blocks.
+// `s` is the lane's block scale; `word` counts 128 columns.
+__device__ __forceinline__ uint32_t quad_word(uint32_t s)
+{
+    const int lane = threadIdx.x & 31;
+    const uint32_t b1 = __shfl_down_sync(0xffffffffu, s, 4), b2 = __shfl_down_sync(0xffffffffu, s, 8),
+                   b3 = __shfl_down_sync(0xffffffffu, s, 12);
+    return (lane & 15) == 0 ? s | b1 << 8 | b2 << 16 | b3 << 24 : 0u;
+}
+
+// x [rows, 8 nvec], row-major scales: one run of vectors (a block never spans two rows)
+template <int DT>
 __global__ void __launch_bounds__(kQThreads) mx_quantize_kernel(const void* x, int64_t total,
-                                                                int32_t nvec, uint32_t* codes,
-                                                                uint8_t* scales)
+                                                                uint32_t* codes, uint8_t* scales)
 {
     pdl_wait();
     const int64_t base = (int64_t)blockIdx.x * (kQThreads * kQVec) + threadIdx.x;
@@ -36,15 +45,43 @@ __global__ void __launch_bounds__(kQThreads) mx_quantize_kernel(const void* x, i
         const uint32_t s = mx_scale_byte(quad_max(mx_amax8(f)));  // quads are whole: 4 | total
         if (v < total) {
             codes[v] = mx_encode8(f, s);
-            if ((threadIdx.x & 3) == 0) {
-                int64_t at = v >> 2;
-                if (TILED) {
-                    const int64_t row = v / nvec;
-                    at = mx_tiled_scale(row, (int)(v - row * nvec) >> 2, nvec >> 2);
-                }
-                scales[at] = (uint8_t)s;
-            }
+            if ((threadIdx.x & 3) == 0) scales[v >> 2] = (uint8_t)s;
         }
+    }
+}
+
+// The same with the scales in tiles, over rows padded to 128 and vectors padded to 16 (`nvecp`):
+// the padding's scales are written as 0, so that every byte of the tiles is defined.
+template <int DT>
+__global__ void __launch_bounds__(kQThreads) mx_quantize_tiled_kernel(const void* x, int64_t rows,
+                                                                      int32_t nvec, int32_t nvecp,
+                                                                      int64_t total,
+                                                                      uint32_t* codes,
+                                                                      uint8_t* scales)
+{
+    pdl_wait();
+    const int64_t base = (int64_t)blockIdx.x * (kQThreads * kQVec) + threadIdx.x;
+    Vec8<DT> q[kQVec];
+    int64_t row[kQVec];
+    int32_t col[kQVec];
+#pragma unroll
+    for (int i = 0; i < kQVec; ++i) {
+        const int64_t v = base + kQThreads * i;
+        row[i] = total <= 0xffffffffll ? (int64_t)((uint32_t)v / (uint32_t)nvecp) : v / nvecp;
+        col[i] = (int32_t)(v - row[i] * nvecp);
+        if (row[i] < rows && col[i] < nvec) q[i].load(x, row[i] * nvec + col[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kQVec; ++i) {
+        const bool in = row[i] < rows && col[i] < nvec;
+        float f[8] = {};
+        if (in) q[i].get(f);
+        const uint32_t s = mx_scale_byte(quad_max(mx_amax8(f)));
+        const uint32_t word = quad_word(s);
+        if (in) codes[row[i] * nvec + col[i]] = mx_encode8(f, s);
+        if ((threadIdx.x & 15) == 0 && base + kQThreads * i < total)
+            *reinterpret_cast<uint32_t*>(scales + mx_tiled_scale(row[i], col[i] >> 2, nvecp >> 2)) =
+                word;
     }
 }
 
@@ -64,6 +101,7 @@ __global__ void __launch_bounds__(kQThreads) mx_scatter_kernel(
         q.get(f);
     }
     const uint32_t s = mx_scale_byte(quad_max(mx_amax8(f)));
+    const uint32_t word = quad_word(s);  // H is a multiple of 128: 16 lanes share a row
     if (v >= total) return;
     const int64_t t = total <= 0xffffffffll ? (int64_t)((uint32_t)v / (uint32_t)nvec) : v / nvec;
     const int32_t c = (int32_t)(v - t * nvec);
@@ -76,18 +114,21 @@ __global__ void __launch_bounds__(kQThreads) mx_scatter_kernel(
             continue;
         }
         codes[(int64_t)r * nvec + c] = w;
-        if ((c & 3) == 0) scales[(int64_t)r * (nvec >> 2) + (c >> 2)] = (uint8_t)s;
+        if ((c & 15) == 0)
+            *reinterpret_cast<uint32_t*>(scales + mx_tiled_scale(r, c >> 2, nvec >> 2)) = word;
     }
     if (tok_codes != nullptr) {
         tok_codes[v] = w;
-        if ((c & 3) == 0) tok_scales[v >> 2] = (uint8_t)s;
+        if ((c & 15) == 0)
+            *reinterpret_cast<uint32_t*>(tok_scales + mx_tiled_scale(t, c >> 2, nvec >> 2)) = word;
     }
 }
 
-template <int DT>
+template <int DT, bool TILED>
 __global__ void __launch_bounds__(kQThreads) mx_dequantize_kernel(const uint32_t* codes,
                                                                   const uint8_t* scales,
-                                                                  int64_t total, void* out)
+                                                                  int64_t total, int32_t nvec,
+                                                                  void* out)
 {
     pdl_wait();
     const int64_t base = (int64_t)blockIdx.x * (kQThreads * kQVec) + threadIdx.x;
@@ -97,7 +138,14 @@ __global__ void __launch_bounds__(kQThreads) mx_dequantize_kernel(const uint32_t
         const int64_t v = base + kQThreads * i;
         if (v < total) {
             c[i] = codes[v];
-            s[i] = scales[v >> 2];
+            int64_t at = v >> 2;
+            if (TILED) {
+                const int64_t row = total <= 0xffffffffll
+                                        ? (int64_t)((uint32_t)v / (uint32_t)nvec)
+                                        : v / nvec;
+                at = mx_tiled_scale(row, (int)(v - row * nvec) >> 2, (nvec + 15) / 16 * 4);
+            }
+            s[i] = scales[at];
         }
     }
 #pragma unroll
@@ -121,17 +169,35 @@ __global__ void __launch_bounds__(kQThreads) mx_dequantize_kernel(const uint32_t
     }
 }
 
-unsigned blocks_of(int64_t total) { return (unsigned)((total + kQThreads * kQVec - 1) / (kQThreads * kQVec)); }
+unsigned blocks_of(int64_t total)
+{
+    return (unsigned)((total + kQThreads * kQVec - 1) / (kQThreads * kQVec));
+}
 
 template <int DT>
-cudaError_t quantize(const void* x, int64_t total, int32_t nvec, bool tiled, uint8_t* codes,
+cudaError_t quantize(const void* x, int64_t rows, int32_t nvec, bool tiled, uint8_t* codes,
                      uint8_t* scales, cudaStream_t st)
 {
     uint32_t* c = reinterpret_cast<uint32_t*>(codes);
-    return tiled ? launch_pdl(mx_quantize_kernel<DT, true>, dim3(blocks_of(total)),
-                              dim3(kQThreads), 0, st, x, total, nvec, c, scales)
-                 : launch_pdl(mx_quantize_kernel<DT, false>, dim3(blocks_of(total)),
-                              dim3(kQThreads), 0, st, x, total, nvec, c, scales);
+    if (!tiled) {
+        const int64_t total = rows * nvec;
+        return launch_pdl(mx_quantize_kernel<DT>, dim3(blocks_of(total)), dim3(kQThreads), 0, st,
+                          x, total, c, scales);
+    }
+    const int32_t nvecp = (nvec + 15) / 16 * 16;
+    const int64_t total = (rows + 127) / 128 * 128 * nvecp;
+    return launch_pdl(mx_quantize_tiled_kernel<DT>, dim3(blocks_of(total)), dim3(kQThreads), 0, st,
+                      x, rows, nvec, nvecp, total, c, scales);
+}
+
+template <int DT>
+cudaError_t dequantize(int64_t rows, int32_t nvec, bool tiled, const uint8_t* codes,
+                       const uint8_t* scales, void* out, cudaStream_t st)
+{
+    const uint32_t* c = reinterpret_cast<const uint32_t*>(codes);
+    const int64_t total = rows * nvec;
+    return launch_pdl(tiled ? mx_dequantize_kernel<DT, true> : mx_dequantize_kernel<DT, false>,
+                      dim3(blocks_of(total)), dim3(kQThreads), 0, st, c, scales, total, nvec, out);
 }
 
 }  // namespace
@@ -139,11 +205,10 @@ cudaError_t quantize(const void* x, int64_t total, int32_t nvec, bool tiled, uin
 cudaError_t launch_mx_quantize(int64_t rows, int32_t K, int dtype, bool tiled, const void* x,
                                uint8_t* codes, uint8_t* scales, cudaStream_t st)
 {
-    const int64_t total = rows * (K / 8);
     switch (dtype) {
-        case MOE_BF16: return quantize<MOE_BF16>(x, total, K / 8, tiled, codes, scales, st);
-        case MOE_F16: return quantize<MOE_F16>(x, total, K / 8, tiled, codes, scales, st);
-        default: return quantize<MOE_F32>(x, total, K / 8, tiled, codes, scales, st);
+        case MOE_BF16: return quantize<MOE_BF16>(x, rows, K / 8, tiled, codes, scales, st);
+        case MOE_F16: return quantize<MOE_F16>(x, rows, K / 8, tiled, codes, scales, st);
+        default: return quantize<MOE_F32>(x, rows, K / 8, tiled, codes, scales, st);
     }
 }
 
@@ -159,22 +224,14 @@ cudaError_t launch_mx_scatter(const moe_cfg& c, const uint16_t* x, const int32_t
                       reinterpret_cast<uint32_t*>(tok_codes), tok_scales, status);
 }
 
-cudaError_t launch_mx_dequantize(int64_t rows, int32_t K, int dtype, const uint8_t* codes,
-                                 const uint8_t* scales, void* out, cudaStream_t st)
+cudaError_t launch_mx_dequantize(int64_t rows, int32_t K, int dtype, bool tiled,
+                                 const uint8_t* codes, const uint8_t* scales, void* out,
+                                 cudaStream_t st)
 {
-    const int64_t total = rows * (K / 8);
-    const uint32_t* c = reinterpret_cast<const uint32_t*>(codes);
-    const dim3 grid(blocks_of(total)), block(kQThreads);
     switch (dtype) {
-        case MOE_BF16:
-            return launch_pdl(mx_dequantize_kernel<MOE_BF16>, grid, block, 0, st, c, scales, total,
-                              out);
-        case MOE_F16:
-            return launch_pdl(mx_dequantize_kernel<MOE_F16>, grid, block, 0, st, c, scales, total,
-                              out);
-        default:
-            return launch_pdl(mx_dequantize_kernel<MOE_F32>, grid, block, 0, st, c, scales, total,
-                              out);
+        case MOE_BF16: return dequantize<MOE_BF16>(rows, K / 8, tiled, codes, scales, out, st);
+        case MOE_F16: return dequantize<MOE_F16>(rows, K / 8, tiled, codes, scales, out, st);
+        default: return dequantize<MOE_F32>(rows, K / 8, tiled, codes, scales, out, st);
     }
 }
 

@@ -589,15 +589,21 @@ def forward_host(cfg: Config, x_host, w_router, w13, w2, logit_bias=None, sel_bi
 
 # ------------------------------------------------------------------ experts in 4 bits
 
-def mx_quantize(x):
+def _mx_tiles(rows: int, K: int):
+    return -(-rows // 128), -(-K // 128), 512
+
+
+def mx_quantize(x, tiled: bool = True):
     """Rows of x [R,K] (bf16, fp16 or fp32, K a multiple of 32) in the microscaled 4-bit format
-    (moe_mx_quantize): (codes [R,K/2], scales [R,K/32]), both uint8."""
+    (moe_mx_quantize): (codes [R,K/2], scales), both uint8. The scales are in the tensor core's
+    tiles, [ceil(R/128), ceil(K/128), 512], as the products take them, or with tiled=False
+    row-major, [R,K/32]."""
     _act(x, "x")
     dev, (R, K) = x.device, x.shape
     codes = torch.empty(R, K // 2, dtype=torch.uint8, device=dev)
-    scales = torch.empty(R, K // 32, dtype=torch.uint8, device=dev)
-    _rc(_call(dev, N.load().moe_mx_quantize, R, K, _DTYPES[x.dtype], 0, _p(x), _p(codes),
-              _p(scales)), "moe_mx_quantize")
+    scales = torch.empty(_mx_tiles(R, K) if tiled else (R, K // 32), dtype=torch.uint8, device=dev)
+    _rc(_call(dev, N.load().moe_mx_quantize, R, K, _DTYPES[x.dtype], int(bool(tiled)), _p(x),
+              _p(codes), _p(scales)), "moe_mx_quantize")
     return codes, scales
 
 
@@ -621,17 +627,19 @@ def mx_weight(w):
 
 
 def mx_dequantize(codes, scales, dtype=torch.bfloat16):
-    """The values of mx_quantize's codes [R,K/2] and scales [R,K/32], rounded to dtype: [R,K]."""
+    """The values of mx_quantize's codes [R,K/2] and scales (in tiles, or row-major [R,K/32]),
+    rounded to dtype: [R,K]."""
     dev = codes.device
     if codes.dim() != 2 or dtype not in _DTYPES or codes.shape[1] % 16:
         raise MoeError(f"codes {tuple(codes.shape)} to {dtype}: [R, K/2] with K a multiple of 32, "
                        "and bf16, fp16 or fp32, are expected")
     R, K = codes.shape[0], 2 * codes.shape[1]
     _need(codes, "codes", torch.uint8, (R, K // 2), dev)
-    _need(scales, "scales", torch.uint8, (R, K // 32), dev)
+    tiled = scales.dim() == 3
+    _need(scales, "scales", torch.uint8, _mx_tiles(R, K) if tiled else (R, K // 32), dev)
     out = torch.empty(R, K, dtype=dtype, device=dev)
-    _rc(_call(dev, N.load().moe_mx_dequantize, R, K, _DTYPES[dtype], _p(codes), _p(scales),
-              _p(out)), "moe_mx_dequantize")
+    _rc(_call(dev, N.load().moe_mx_dequantize, R, K, _DTYPES[dtype], int(tiled), _p(codes),
+              _p(scales), _p(out)), "moe_mx_dequantize")
     return out
 
 
@@ -647,8 +655,8 @@ def _mx_need(w, name, shape, dev):
 
 def mx_grouped_gemm(codes, scales, offsets, w_codes, w_scales, swiglu: bool = False, out=None,
                     status=None, check: bool = True):
-    """Rows in 4 bits (mx_quantize), grouped by offsets [E+1], times 4-bit weights (mx_weight of
-    [E,N,K]): [R,N] bf16, or with swiglu silu(first N/2 columns) * last N/2, [R,N/2]
+    """Rows in 4 bits (mx_quantize, scales in tiles), grouped by offsets [E+1], times 4-bit weights
+    (mx_weight of [E,N,K]): [R,N] bf16, or with swiglu silu(first N/2 columns) * last N/2, [R,N/2]
     (moe_mx_grouped_gemm). Rows outside every group are left as they were in out."""
     dev = codes.device
     if w_codes.dim() != 3 or codes.dim() != 2:
@@ -658,7 +666,7 @@ def mx_grouped_gemm(codes, scales, offsets, w_codes, w_scales, swiglu: bool = Fa
     if n % (256 if swiglu else 128) or K % 128:
         raise MoeError(f"N {n} and K {K}: multiples of {256 if swiglu else 128} and 128")
     _need(codes, "codes", torch.uint8, (R, K // 2), dev)
-    _need(scales, "scales", torch.uint8, (R, K // 32), dev)
+    _need(scales, "scales", torch.uint8, _mx_tiles(R, K), dev)
     _need(offsets, "offsets", torch.int32, (E + 1,), dev)
     _mx_need((w_codes, w_scales), "w", (E, n, K), dev)
     shape = (R, n // 2 if swiglu else n)

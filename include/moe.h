@@ -493,23 +493,24 @@ MOE_API int moe_dropout(int64_t T, int32_t H, int32_t dtype, double p, const voi
  * to nearest even, saturated at +-6. A block with an infinity or a NaN gets the scale 255 (NaN)
  * and codes 0, and every result that meets it is NaN.
  *
- * Weights keep their scales in the tensor core's tiles: for a matrix of N rows and K columns
- * (both multiples of 128) tile (N / 128, K / 128) is 512 bytes, the scale of row r and block b
- * of the tile at 16 (r % 32) + 4 (r / 32) + b.
+ * The products take scales in the tensor core's tiles: 128 rows by 4 blocks (128 columns) are
+ * 512 consecutive bytes, the scale of row r and block b of the tile at
+ * 16 (r % 32) + 4 (r / 32) + b; the tiles of [rows, K] are [ceil(rows / 128), ceil(K / 128), 512].
  */
 
 /*
- * x [rows, K] of `dtype` -> codes [rows, K / 2], scales [rows, K / 32], or with tiled = 1 the
- * scales in tiles, [rows / 128, K / 128, 512] (a batch of matrices of N rows each, N a multiple
- * of 128, is one call with rows = batch * N). K % 32 == 0, tiled: rows and K % 128 == 0;
- * 0 <= rows, rows * K < 2^42, K <= 2^20.
+ * x [rows, K] of `dtype` -> codes [rows, K / 2] and the scales, row-major [rows, K / 32] with
+ * tiled = 0, in tiles with tiled = 1 (those of padding rows and blocks are 0). A batch of
+ * matrices of N rows each, N a multiple of 128, is one call with rows = batch * N.
+ * K % 32 == 0, 32 <= K <= 2^20, 0 <= rows, rows * K < 2^42.
  */
 MOE_API int moe_mx_quantize(int64_t rows, int32_t K, int32_t dtype, int32_t tiled, const void* x,
                             uint8_t* codes, uint8_t* scales, void* stream);
 
-/* The values that codes and row-major scales stand for, rounded to `dtype`. */
-MOE_API int moe_mx_dequantize(int64_t rows, int32_t K, int32_t dtype, const uint8_t* codes,
-                              const uint8_t* scales, void* out, void* stream);
+/* The values that codes and scales stand for, rounded to `dtype`: out [rows, K]. */
+MOE_API int moe_mx_dequantize(int64_t rows, int32_t K, int32_t dtype, int32_t tiled,
+                              const uint8_t* codes, const uint8_t* scales, void* out,
+                              void* stream);
 
 /*
  * Grouped product of 4-bit rows and 4-bit weights, fp32 accumulation on the tensor cores:
@@ -519,10 +520,10 @@ MOE_API int moe_mx_dequantize(int64_t rows, int32_t K, int32_t dtype, const uint
  * A row's result depends on that row and the weights alone, with K in a fixed order. Rows
  * outside every group are left as they were.
  *
- *  a_codes [rows, K / 2], a_scales [rows, K / 32]  (from moe_mx_quantize).
+ *  a_codes [rows, K / 2], a_scales in tiles  (from moe_mx_quantize).
  *  offsets  [groups + 1] int32 device, or NULL (groups = 1: all rows). An offset outside
  *           [0, rows] or below its predecessor counts in status[MOE_ST_BAD_ROWS] and is clamped.
- *  b_codes  [groups, N, K / 2], b_scales [groups, N / 128, K / 128, 512].
+ *  b_codes  [groups, N, K / 2], b_scales in tiles, [groups, N / 128, K / 128, 512].
  *  out      [rows, N] bf16, or [rows, N / 2] with swiglu.
  *  status   int32[MOE_STATUS_WORDS] device, cleared first; may be NULL.
  * 0 <= rows < 2^31, 1 <= groups <= 1024, N and K multiples of 128 from 128 to 32768 (swiglu:

@@ -58,6 +58,11 @@ def untile(tiled):
     return t.reshape(*lead, n * 128, b * 4)
 
 
+def rows_of(tiled, R, K):
+    """Row-major scales [R, K/32] from the tiles of [R, K] (padding dropped)."""
+    return untile(tiled)[:R, :K // 32]
+
+
 def product64(a, w, offsets, swiglu):
     """(out, magnitude of the sums) over groups of rows; NaN-free inputs. With swiglu both are
     of silu(gate) * up, its magnitude the first-order propagation of the sums'."""

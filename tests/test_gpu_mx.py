@@ -46,13 +46,19 @@ def test_quantize_codes_and_values(dt, R, K):
         x[2, 16:32] = 0
         x[1, :32] = torch.finfo(TYPES[dt]).smallest_normal
         x[1, 0] = torch.finfo(TYPES[dt]).max
-    codes, scales = moe.mx_quantize(x)
+    codes, scales = moe.mx_quantize(x, tiled=False)
     ref, rs = M.quantize64(x)
     assert torch.equal(scales, rs)
     assert torch.equal(M.unpack(codes), ref)
+    c2, tiles = moe.mx_quantize(x)
+    assert torch.equal(c2, codes)
+    pad = torch.zeros(-(-R // 128) * 128, -(-K // 128) * 4, dtype=torch.uint8, device=DEV)
+    pad[:R, :K // 32] = rs
+    assert torch.equal(M.untile(tiles), pad)  # the padding's scales are 0
     for out in TYPES.values():
-        got = moe.mx_dequantize(codes, scales, out)
-        assert torch.equal(got, M.values64(codes, scales).to(out))
+        want = M.values64(codes, scales).to(out)
+        assert torch.equal(moe.mx_dequantize(codes, scales, out), want)
+        assert torch.equal(moe.mx_dequantize(codes, tiles, out), want)
 
 
 def test_quantize_subnormals_and_extremes():
@@ -60,7 +66,7 @@ def test_quantize_subnormals_and_extremes():
     x = torch.zeros(6, 32, device=DEV)
     x[0, 1], x[1, 2], x[2, 3] = 2.0 ** -149, 2.0 ** -128, 1.5 * 2.0 ** -126
     x[3], x[4, 0], x[5, 5] = torch.finfo(torch.float32).max, 2.0 ** -125, 5 * 2.0 ** -127
-    codes, scales = moe.mx_quantize(x)
+    codes, scales = moe.mx_quantize(x, tiled=False)
     ref, rs = M.quantize64(x)
     assert torch.equal(scales, rs) and torch.equal(M.unpack(codes), ref)
 
@@ -68,7 +74,7 @@ def test_quantize_subnormals_and_extremes():
 def test_non_finite_blocks():
     x = torch.ones(4, 128, device=DEV)
     x[0, 5], x[1, 40], x[2, 127] = float("nan"), float("inf"), float("-inf")
-    codes, scales = moe.mx_quantize(x)
+    codes, scales = moe.mx_quantize(x, tiled=False)
     want = torch.full((4, 4), 125, dtype=torch.uint8)
     want[0, 0] = want[1, 1] = want[2, 3] = 255
     assert torch.equal(scales.cpu(), want)
@@ -84,7 +90,7 @@ def test_weights_keep_their_scales_in_tiles(shape):
     codes, tiled = moe.mx_weight(w)
     ref, rs = M.quantize64(w)
     assert torch.equal(M.unpack(codes), ref) and torch.equal(M.untile(tiled), rs)
-    c2, s2 = moe.mx_quantize(w.view(-1, shape[-1]))
+    c2, s2 = moe.mx_quantize(w.view(-1, shape[-1]), tiled=False)
     assert torch.equal(c2.view_as(codes), codes) and torch.equal(s2.view_as(rs), rs)
 
 
@@ -101,7 +107,7 @@ def make_product(sizes, N_, K, seed=0, start=0, extra=0):
 
 
 def check_product(out, x, w, off, swiglu, K):
-    a = M.values64(*moe.mx_quantize(x))
+    a = M.values64(*moe.mx_quantize(x, tiled=False))
     wc, ws = moe.mx_weight(w)
     ref, mag = M.product64(a, M.values64(wc, M.untile(ws)), off, swiglu)
     tol = 2.0 ** -8 * ref.abs() + K * 2.0 ** -24 * mag + (2.0 ** -17 * ref.abs() if swiglu else 0)
@@ -154,12 +160,12 @@ def test_a_row_keeps_its_bits_anywhere():
     K, n = 896, 512
     w = moe.mx_weight(rows_like((3, n, K), 5) * 0.02)
     x = rows_like((600, K), 6)
-    c, s = moe.mx_quantize(x)
 
     def run(rows, off, glu):
         i = torch.tensor(rows, device=DEV)
-        return moe.mx_grouped_gemm(c[i], s[i], torch.tensor(off, dtype=torch.int32, device=DEV),
-                                   *w, swiglu=glu)
+        return moe.mx_grouped_gemm(*moe.mx_quantize(x[i]),
+                                   torch.tensor(off, dtype=torch.int32, device=DEV), *w,
+                                   swiglu=glu)
 
     for glu in (False, True):
         full = run(list(range(600)), [0, 100, 500, 600], glu)
@@ -234,17 +240,16 @@ def layer(name, T, mask=False, **over):
 
 def staged(cfg, d, q, dest, offsets):
     """The stage by its public parts: quantise, gather, product, quantise, product."""
-    c, s = moe.mx_quantize(d["x"])
     n = int(offsets[-1])
     tok = torch.empty(n, dtype=torch.long, device=DEV)
     t, j = (dest >= 0).nonzero(as_tuple=True)
     tok[dest[t, j].long()] = t
-    h = moe.mx_grouped_gemm(c[tok], s[tok], offsets, *q["w13"], swiglu=True)
+    h = moe.mx_grouped_gemm(*moe.mx_quantize(d["x"][tok]), offsets, *q["w13"], swiglu=True)
     y = moe.mx_grouped_gemm(*moe.mx_quantize(h), offsets, *q["w2"])
     if not cfg.I_shared:
         return y, None
     one = torch.tensor([0, cfg.T], dtype=torch.int32, device=DEV)
-    hs = moe.mx_grouped_gemm(c, s, one, q["w13_s"][0][None], q["w13_s"][1][None], swiglu=True)
+    hs = moe.mx_grouped_gemm(*moe.mx_quantize(d["x"]), one, q["w13_s"][0][None], q["w13_s"][1][None], swiglu=True)
     return y, moe.mx_grouped_gemm(*moe.mx_quantize(hs), one, q["w2_s"][0][None], q["w2_s"][1][None])
 
 
@@ -274,7 +279,7 @@ def test_layer_near_the_64_bit_layer_of_its_values():
     logits, ids, tw = moe.route(cfg, x=d["x"], w_router=d["w_router"], logit_bias=d["logit_bias"])
     offsets, perm, dest, _ = moe.permute(cfg, ids, want_x_perm=False)
     y, _ = moe.mx_grouped_ffn(cfg, d["x"], dest, offsets, **q)
-    a = M.values64(*moe.mx_quantize(d["x"]))[perm.long()]
+    a = M.values64(*moe.mx_quantize(d["x"], tiled=False))[perm.long()]
     off = offsets.tolist()
     ref = torch.zeros(y.shape, dtype=torch.float64, device=DEV)
     for e in range(cfg.E):

@@ -56,16 +56,16 @@ def test_quantize_refusals(lib):
         return lib.moe_mx_quantize(rows, K, dt, tiled, x, c, s, None)
 
     for over in (dict(rows=-1), dict(K=0), dict(K=48), dict(K=1 << 21), dict(dt=3), dict(dt=-1),
-                 dict(rows=1 << 40, K=64), dict(rows=100, K=128, tiled=1),
-                 dict(rows=128, K=96, tiled=1)):
+                 dict(rows=1 << 40, K=64)):
         assert q(**over) == N.MOE_ERR_SHAPE, over
-    for over in (dict(tiled=2), dict(x=None), dict(c=None), dict(s=None), dict(x=ODD), dict(c=ODD)):
+    for over in (dict(tiled=2), dict(x=None), dict(c=None), dict(s=None), dict(x=ODD), dict(c=ODD),
+                 dict(s=ODD, tiled=1)):
         assert q(**over) == N.MOE_ERR_ARG, over
     assert q(rows=0, x=None) == N.MOE_OK
-    assert lib.moe_mx_dequantize(4, 48, 0, FAKE, FAKE, FAKE, None) == N.MOE_ERR_SHAPE
-    assert lib.moe_mx_dequantize(4, 64, 5, FAKE, FAKE, FAKE, None) == N.MOE_ERR_SHAPE
-    assert lib.moe_mx_dequantize(4, 64, 0, FAKE, None, FAKE, None) == N.MOE_ERR_ARG
-    assert lib.moe_mx_dequantize(4, 64, 0, ODD, FAKE, FAKE, None) == N.MOE_ERR_ARG
+    assert lib.moe_mx_dequantize(4, 48, 0, 0, FAKE, FAKE, FAKE, None) == N.MOE_ERR_SHAPE
+    assert lib.moe_mx_dequantize(4, 64, 5, 0, FAKE, FAKE, FAKE, None) == N.MOE_ERR_SHAPE
+    assert lib.moe_mx_dequantize(4, 64, 0, 1, FAKE, None, FAKE, None) == N.MOE_ERR_ARG
+    assert lib.moe_mx_dequantize(4, 64, 0, 0, ODD, FAKE, FAKE, None) == N.MOE_ERR_ARG
 
 
 def test_product_refusals(lib):
@@ -116,7 +116,8 @@ def test_layer_refusals(lib):
 
 def test_binding_refusals():
     x = torch.zeros(4, 128, dtype=torch.bfloat16)
-    c, s = torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, 4, dtype=torch.uint8)
+    c, s = torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(1, 1, 512, dtype=torch.uint8)
+    flat = torch.zeros(4, 4, dtype=torch.uint8)
     wc = torch.zeros(2, 256, 64, dtype=torch.uint8)
     ws = torch.zeros(2, 2, 1, 512, dtype=torch.uint8)
     off = torch.zeros(3, dtype=torch.int32)
@@ -124,11 +125,12 @@ def test_binding_refusals():
            lambda: moe.mx_quantize(x.t()), lambda: moe.mx_quantize(x),  # not on a GPU
            lambda: moe.mx_weight(x), lambda: moe.mx_weight(x.int()),
            lambda: moe.mx_weight(torch.zeros(128, 192)),
-           lambda: moe.mx_dequantize(c, s, torch.int8), lambda: moe.mx_dequantize(c, s[:, :3]),
+           lambda: moe.mx_dequantize(c, s, torch.int8), lambda: moe.mx_dequantize(c, flat[:, :3]),
            lambda: moe.mx_dequantize(c[:, :8].contiguous(), s),
            lambda: moe.mx_grouped_gemm(c, s, off[:2], wc, ws),
            lambda: moe.mx_grouped_gemm(c, s, off, wc, ws.flatten(2)),
            lambda: moe.mx_grouped_gemm(c, s.int(), off, wc, ws),
+           lambda: moe.mx_grouped_gemm(c, flat, off, wc, ws),  # row-major scales
            lambda: moe.mx_grouped_gemm(c, s, off, wc[:, :128].contiguous(), ws, swiglu=True),
            lambda: moe.mx_grouped_gemm(c, s, off.long(), wc, ws),
            lambda: moe.mx_grouped_ffn(moe.Config(T=4, H=128, E=2, K=1, I=128), x,
