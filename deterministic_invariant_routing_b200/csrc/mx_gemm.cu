@@ -119,10 +119,42 @@ __device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t des
                  : "memory");
 }
 
+// True in one lane of a converged warp. The loading and issuing roles run as whole warps whose
+// loop state is the same in every lane, and only the instructions themselves are one lane's: the
+// compiler then keeps descriptors and addresses in uniform registers, which is where tcgen05 and
+// TMA instructions take them from. As loops of a single thread (`lane == 0`) every operand was
+// moved there per instruction, and issuing a k-block took 1400 cycles instead of 512.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(p));
+    return p != 0;
+}
+
+// a value that every lane of the warp holds, known to be the same in all of them
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // descriptor of such a 512-byte tile: no swizzle, groups of 8 rows 128 bytes apart
 __device__ __forceinline__ uint64_t scale_desc(uint32_t saddr)
 {
     return (uint64_t)((saddr >> 4) & 0x3fffu) | (uint64_t)(128u >> 4) << 32 | (uint64_t)1u << 46;
+}
+
+// silu(g) * u with the hardware's base-2 exponential and reciprocal (a few ulp of fp32, far below
+// the bf16 rounding that follows): six instructions. The epilogue has 16384 of these per CTA and
+// tile beside a main loop a quarter as long as the bf16 kernel's; with the IEEE reciprocal and
+// the denormal-safe exponential it took about 11000 cycles a tile and bound the product.
+// g -> -inf gives -0; an overflowed exponential gives a zero reciprocal.
+__device__ __forceinline__ float swiglu_fast(float g, float u)
+{
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return g * r * u;
 }
 
 template <int MODE>
@@ -156,9 +188,9 @@ __global__ void __launch_bounds__(kXThreads, 1)
     int32_t* prefix = reinterpret_cast<int32_t*>(misc + 4);  // [groups + 1] row tiles before g
     int32_t* offs = prefix + (args.groups + 1);              // [groups + 1]
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int G = args.groups;
-    const uint32_t rank = cluster_ctarank();
+    const uint32_t rank = blockIdx.x & 1;  // clusters are pairs of consecutive blocks
     const bool leader = rank == 0;
     const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
 
@@ -219,8 +251,14 @@ __global__ void __launch_bounds__(kXThreads, 1)
     tc_fence_before();
     cluster_sync();
     tc_fence_after();
-    const uint32_t tmem_base = misc[0];
-    const int total = prefix[G] * args.n_tiles;
+    const uint32_t tmem_base = (uint32_t)uniform((int)misc[0]);
+    const int total = uniform(prefix[G] * args.n_tiles);
+    // a bounded wait of a whole warp: true when every lane's completed
+    auto wait_warp = [&](uint32_t bar, uint32_t parity, bool honour_abort = true) -> bool {
+        return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, args.status,
+                                                    honour_abort));
+    };
+    auto aborted = [&]() -> bool { return __any_sync(0xffffffffu, *abort_flag != 0); };
     auto decode = [&](int t) -> MxTile {
         MxTile ti;
         const int mt = t / args.n_tiles;
@@ -240,32 +278,32 @@ __global__ void __launch_bounds__(kXThreads, 1)
 
     if (warp == 0) {
         // -------------------------------------------------------------- TMA producer
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0, armed = 0, armed_phase = 0;
-            const uint32_t fb0 = mapa_shared(full_bar(0), 0);
-            const int kc = args.k / 128;  // scale tiles along K
-            for (int t = cluster; t < total && !*abort_flag; t += nclusters) {
-                const MxTile ti = decode(t);
-                const int arow = (int)ti.row0 + (int)rank * XH;
-                const int b0 = ti.g * args.sb_tiles + (kGlu ? ti.n : 2 * ti.n);  // 128-row tiles
-                const int b1 = kGlu ? b0 + args.half / 128 : b0 + 1;
-                const int brow = (leader ? b0 : b1) * 128;
-                // a whole tile's rows come in one box; of a partial one only the 32-row boxes
-                // with rows of the group (decode-sized groups read few rows)
-                const uint32_t mine = mx_boxes(ti, rank), other = mx_boxes(ti, rank ^ 1u);
-                const uint32_t bytes = 2 * (kXB + kXSA + kXSB) +
-                                       kXBox * (uint32_t)(__popc(mine) + __popc(other));
-                const int sa = (int)(ti.row0 / 128 + rank) * kc;
-                bool ok = true;
-                for (int kb = 0; kb < args.k_blocks; ++kb) {
-                    if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, args.status)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t fb = fb0 + 8u * (uint32_t)stage;
+        int stage = 0;
+        uint32_t phase = 0, armed = 0, armed_phase = 0;
+        const uint32_t fb0 = (uint32_t)uniform((int)mapa_shared(full_bar(0), 0));
+        const int kc = args.k / 128;  // scale tiles along K
+        for (int t = cluster; t < total && !aborted(); t += nclusters) {
+            const MxTile ti = decode(t);
+            const int arow = uniform((int)ti.row0) + (int)rank * XH;
+            const int b0 = uniform(ti.g) * args.sb_tiles + uniform(kGlu ? ti.n : 2 * ti.n);
+            const int b1 = kGlu ? b0 + args.half / 128 : b0 + 1;  // 128-row tiles of B
+            const int brow = (leader ? b0 : b1) * 128;
+            // a whole tile's rows come in one box; of a partial one only the 32-row boxes with
+            // rows of the group (decode-sized groups read few rows)
+            const uint32_t mine = (uint32_t)uniform((int)mx_boxes(ti, rank));
+            const uint32_t other = (uint32_t)uniform((int)mx_boxes(ti, rank ^ 1u));
+            const uint32_t bytes = 2 * (kXB + kXSA + kXSB) +
+                                   kXBox * (uint32_t)(__popc(mine) + __popc(other));
+            const int sa = (arow >> 7) * kc, sb0 = b0 * kc, sb1 = b1 * kc;
+            bool ok = true;
+            for (int kb = 0; kb < args.k_blocks; ++kb) {
+                if (!wait_warp(empty_bar(stage), phase ^ 1u)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t fb = fb0 + 8u * (uint32_t)stage, ss = (uint32_t)stage;
+                if (elect_one()) {
                     if (leader) mbar_expect_tx(full_bar(stage), bytes);
-                    const uint32_t ss = (uint32_t)stage;
                     if (mine == 15u) {
                         tma_load_2d_pair(sA0 + ss * kXA, &tmA, kb * (XK / 2), arow, fb);
                     } else {
@@ -275,29 +313,28 @@ __global__ void __launch_bounds__(kXThreads, 1)
                                 tma_load_2d_pair(sA0 + ss * kXA + j * kXBox, &tmA32, kb * (XK / 2),
                                                  arow + 32 * j, fb);
                     }
-                    tma_load_2d_pair(sSA0 + ss * kXSA, &tmSA, 0, sa + 2 * kb, fb);
                     tma_load_2d_pair(sB0 + ss * kXB, &tmB, kb * (XK / 2), brow, fb);
-                    tma_load_2d_pair(sSB0 + ss * kXSB, &tmSB, 0, b0 * kc + 2 * kb, fb);
-                    tma_load_2d_pair(sSB0 + ss * kXSB + 1024u, &tmSB, 0, b1 * kc + 2 * kb, fb);
-                    armed |= 1u << stage;
-                    armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
-                    if (++stage == kXS) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                    tma_load_2d_pair(sSA0 + ss * kXSA, &tmSA, 0, sa + 2 * kb, fb);
+                    tma_load_2d_pair(sSB0 + ss * kXSB, &tmSB, 0, sb0 + 2 * kb, fb);
+                    tma_load_2d_pair(sSB0 + ss * kXSB + 1024u, &tmSB, 0, sb1 + 2 * kb, fb);
                 }
-                if (!ok) break;
+                __syncwarp();
+                armed |= 1u << stage;
+                armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
+                if (++stage == kXS) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
             }
-            pdl_trigger();
-            if (*abort_flag && leader) {
-                for (int s = 0; s < kXS; ++s)
-                    if (armed & (1u << s))
-                        wait_bounded(full_bar(s), (armed_phase >> s) & 1u, abort_flag,
-                                     args.status, false);
-            }
+            if (!ok) break;
+        }
+        pdl_trigger();
+        if (aborted() && leader) {
+            for (int s = 0; s < kXS; ++s)
+                if (armed & (1u << s)) wait_warp(full_bar(s), (armed_phase >> s) & 1u, false);
         }
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        if (leader) {
             // ---------------------------------------------------------- MMA issuer
             const uint64_t ad0 = sw128_desc(sA0), bd0 = sw128_desc(sB0);
             const uint64_t sad0 = scale_desc(sSA0), sbd0 = scale_desc(sSB0);
@@ -305,18 +342,15 @@ __global__ void __launch_bounds__(kXThreads, 1)
             int stage = 0;
             uint32_t phase = 0;
             int i = 0;
-            for (int t = cluster; t < total && !*abort_flag; t += nclusters, ++i) {
+            for (int t = cluster; t < total && !aborted(); t += nclusters, ++i) {
                 const int acc = i & 1;
-                if (!wait_bounded(tempty_bar(acc), (((uint32_t)i >> 1) & 1u) ^ 1u, abort_flag,
-                                  args.status))
-                    break;
-                if (i > 0 && !wait_bounded(tover, ((uint32_t)i - 1u) & 1u, abort_flag, args.status))
-                    break;
+                if (!wait_warp(tempty_bar(acc), (((uint32_t)i >> 1) & 1u) ^ 1u)) break;
+                if (i > 0 && !wait_warp(tover, ((uint32_t)i - 1u) & 1u)) break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + (acc ? kXAcc1 : 0u);
                 bool ok = true;
                 for (int kb = 0; kb < args.k_blocks; ++kb) {
-                    if (!wait_bounded(full_bar(stage), phase, abort_flag, args.status)) {
+                    if (!wait_warp(full_bar(stage), phase)) {
                         ok = false;
                         break;
                     }
@@ -324,34 +358,38 @@ __global__ void __launch_bounds__(kXThreads, 1)
                     const uint64_t st = (uint64_t)(uint32_t)stage;
                     const uint64_t ad = ad0 + st * (kXA >> 4), bd = bd0 + st * (kXB >> 4);
                     const uint64_t sad = sad0 + st * (kXSA >> 4), sbd = sbd0 + st * (kXSB >> 4);
-                    const int chunks = args.k - kb * XK >= XK ? 2 : 1;  // of 128 columns
-                    for (int c = 0; c < chunks; ++c) {
-                        tmem_cp_scales_pair(tsa + 4u * c, sad + (uint64_t)(c * (512 >> 4)));
-                        tmem_cp_scales_pair(tsb + 8u * c, sbd + (uint64_t)(c * (512 >> 4)));
-                        tmem_cp_scales_pair(tsb + 8u * c + 4u,
-                                            sbd + (uint64_t)((1024 + c * 512) >> 4));
+                    const bool both = args.k - kb * XK >= XK;  // two chunks of 128 columns
+                    if (elect_one()) {
+                        auto copy = [&](uint32_t c) {
+                            tmem_cp_scales_pair(tsa + 4u * c, sad + (uint64_t)(c * (512 >> 4)));
+                            tmem_cp_scales_pair(tsb + 8u * c, sbd + (uint64_t)(c * (512 >> 4)));
+                            tmem_cp_scales_pair(tsb + 8u * c + 4u,
+                                                sbd + (uint64_t)((1024 + c * 512) >> 4));
+                        };
+                        auto mma = [&](uint32_t c, uint32_t accumulate) {
+                            mma_mxf4_pair(d, ad + 4u * c, bd + 4u * c, mx_idesc(XM, XN, 0),
+                                          tsa + 4u * c, tsb + 8u * c, accumulate);
+                            mma_mxf4_pair(d, ad + 4u * c + 2u, bd + 4u * c + 2u,
+                                          mx_idesc(XM, XN, 2), tsa + 4u * c, tsb + 8u * c, 1u);
+                        };
+                        copy(0);
+                        if (both) copy(1);
+                        mma(0, kb != 0 ? 1u : 0u);
+                        if (both) mma(1, 1u);
+                        mma_commit_pair_mc(empty_bar(stage), kXPair);
+                        if (kb == args.k_blocks - 1) mma_commit_pair_mc(tfull_bar(acc), kXPair);
                     }
-                    for (int c = 0; c < chunks; ++c) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint64_t step = (uint64_t)(2 * (2 * c + h));
-                            mma_mxf4_pair(d, ad + step, bd + step,
-                                          h ? mx_idesc(XM, XN, 2) : mx_idesc(XM, XN, 0),
-                                          tsa + 4u * c, tsb + 8u * c,
-                                          (kb | c | h) != 0 ? 1u : 0u);
-                        }
-                    }
-                    mma_commit_pair_mc(empty_bar(stage), kXPair);
+                    __syncwarp();
                     if (++stage == kXS) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
                 if (!ok) break;
-                mma_commit_pair_mc(tfull_bar(acc), kXPair);
             }
-            mma_commit_pair(drain);
-            wait_bounded(drain, 0u, abort_flag, args.status, false);
+            if (elect_one()) mma_commit_pair(drain);
+            __syncwarp();
+            wait_warp(drain, 0u, false);
         }
     } else {
         // -------------------------------------------------------------- epilogue
@@ -427,7 +465,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
                         float hv[2];
 #pragma unroll
                         for (int h2 = 0; h2 < 2; ++h2)
-                            hv[h2] = swiglu(__uint_as_float(g[2 * j + h2]),
+                            hv[h2] = swiglu_fast(__uint_as_float(g[2 * j + h2]),
                                             __uint_as_float(u[2 * j + h2]));
                         pk[j] = bf16x2_rne(hv[0], hv[1]);
                     }
