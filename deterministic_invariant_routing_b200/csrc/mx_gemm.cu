@@ -201,9 +201,9 @@ __global__ void __launch_bounds__(kXThreads, 1)
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(tfull_bar(a), 1);
-            mbar_init(tempty_bar(a), 2 * kXEpiWarps * 32);
+            mbar_init(tempty_bar(a), 2 * kXEpiWarps);  // a warp of either CTA each
         }
-        mbar_init(tover, kXEpiWarps * 32);  // half of each CTA's epilogue warps
+        mbar_init(tover, kXEpiWarps);  // half of each CTA's epilogue warps
         mbar_init(drain, 1);
         misc[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -432,12 +432,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
         int i = 0;
         for (int t = cluster; t < total && !*abort_flag; t += nclusters, ++i) {
             const MxTile ti = decode(t);
-            int ok = 1;
             const int acc = i & 1;
-            if (lane == 0)
-                ok = wait_bounded(tfull_bar(acc), ((uint32_t)i >> 1) & 1u, abort_flag, args.status);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) break;
+            if (!wait_warp(tfull_bar(acc), ((uint32_t)i >> 1) & 1u)) break;
             tc_fence_after();
             const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (acc ? kXAcc1 : 0u);
             // the shared columns are the first accumulator's last chunk and the second's first:
@@ -445,7 +441,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
             const bool over = half == (acc ? 0 : 1);
             auto release_shared = [&]() {
                 tc_fence_before();
-                mbar_arrive_cluster(tover_leader);
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(tover_leader);
             };
             const int64_t grow = ti.row0 + (int64_t)rank * XH + row;
             const bool valid = grow >= ti.row_beg && grow < ti.row_end;
@@ -456,9 +453,15 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 for (int k = 0; k < 2; ++k) {
                     const int c = half ? 96 - 32 * k : 32 * k;
                     uint32_t g[32], u[32];
-                    tmem_ld32(tbase + (uint32_t)c, g);
-                    tmem_ld32(tbase + (uint32_t)(XN / 2 + c), u);
-                    if (k == 0 && over) release_shared();
+                    if (half) {  // the shared columns first: gates in one half, ups in the other
+                        tmem_ld32(tbase + (uint32_t)(XN / 2 + c), u);
+                        if (k == 0 && over) release_shared();
+                        tmem_ld32(tbase + (uint32_t)c, g);
+                    } else {
+                        tmem_ld32(tbase + (uint32_t)c, g);
+                        if (k == 0 && over) release_shared();
+                        tmem_ld32(tbase + (uint32_t)(XN / 2 + c), u);
+                    }
                     uint32_t pk[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
@@ -514,7 +517,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 }
             }
             tc_fence_before();
-            mbar_arrive_cluster(acc ? tempty_leader1 : tempty_leader0);
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(acc ? tempty_leader1 : tempty_leader0);
         }
         if (lane == 0) bulk_wait_all();
     }
