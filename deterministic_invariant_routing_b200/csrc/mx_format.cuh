@@ -70,6 +70,26 @@ __device__ __forceinline__ uint32_t mx_encode8(const float (&v)[8], uint32_t s)
     return mx_codes8(w);
 }
 
+// 8 codes to the values they stand for (exact: e2m1 in fp16)
+__device__ __forceinline__ void mx_decode8(uint32_t codes, float (&f)[8])
+{
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(codes));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 v = *reinterpret_cast<const __half2*>(&h[i]);
+        f[2 * i] = __low2float(v);
+        f[2 * i + 1] = __high2float(v);
+    }
+}
+
 // Offset of the scale of (row, block) in the tensor core's tiles: 128 rows by 4 blocks of 32
 // (128 columns) are 512 consecutive bytes, row r at 16 (r % 32) + 4 (r / 32), its 4 blocks in
 // order; tiles follow along the row first. `row` counts over all matrices of a batch (each a

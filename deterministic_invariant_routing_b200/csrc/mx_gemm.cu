@@ -47,7 +47,7 @@ constexpr uint32_t kXStage = kXA + kXB + kXSA + kXSB;
 constexpr int kXS = 5;                  // stages
 constexpr uint32_t kXBox = 32 * XK / 2; // a 32-row box of A
 constexpr int kXEpiWarps = 8;
-constexpr uint32_t kXEpi = kXEpiWarps * 2 * 2048;
+constexpr uint32_t kXEpi = kXEpiWarps * 4096;  // a 32-row x 64-column bf16 tile per epilogue warp
 constexpr int kXThreads = 32 * (2 + kXEpiWarps);
 constexpr int kXBars = 2 * kXS + 6;
 constexpr uint32_t kXCols = 512;        // TMEM columns
@@ -142,6 +142,32 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, 
 __device__ __forceinline__ uint64_t scale_desc(uint32_t saddr)
 {
     return (uint64_t)((saddr >> 4) & 0x3fffu) | (uint64_t)(128u >> 4) << 32 | (uint64_t)1u << 46;
+}
+
+// 64 consecutive fp32 columns of this thread's TMEM lane, waited for as in tmem_ld32
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
+        "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, "
+        "%35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, "
+        "%52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63},  "
+        "[%64];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]),
+          "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]),
+          "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+          "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]),
+          "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]),
+          "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr)
+        : "memory");
 }
 
 // silu(g) * u with the hardware's base-2 exponential and reciprocal (a few ulp of fp32, far below
@@ -399,34 +425,36 @@ __global__ void __launch_bounds__(kXThreads, 1)
         const uint32_t tempty_leader0 = mapa_shared(tempty_bar(0), 0);
         const uint32_t tempty_leader1 = mapa_shared(tempty_bar(1), 0);
         const uint32_t tover_leader = mapa_shared(tover, 0);
+        // Output: 32 rows x 64 columns of bf16 (128 bytes a row, 128-byte swizzle) through shared
+        // memory and one TMA store where all 32 rows belong to the group, else row by row.
         const uint32_t ebuf = sE0 + (uint32_t)(warp - 2) * 4096u;
-        uint32_t eb = 0;
-        const uint32_t erow = (uint32_t)lane * 64u, eswz = ((uint32_t)lane >> 1) & 3u;
-        auto store_block = [&](const uint32_t (&pk)[16], bool full_blk, bool valid, int row_blk,
-                               int col, uint16_t* dst_row) {
-            if (full_blk) {
-                const uint32_t b = ebuf + eb * 2048u;
-                if (lane == 0) bulk_wait_read<1>();
-                __syncwarp();
+        const uint32_t erow = ebuf + (uint32_t)lane * 128u, eswz = (uint32_t)lane & 7u;
+        auto tile_free = [&]() {
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+        };
+        // 32 packed columns to the lower (0) or upper (1) half of this lane's row
+        auto put32 = [&](const uint32_t* pk, int upper) {
 #pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                     b + erow + ((((uint32_t)v) ^ eswz) << 4)),
-                                 "r"(pk[4 * v]), "r"(pk[4 * v + 1]), "r"(pk[4 * v + 2]),
-                                 "r"(pk[4 * v + 3])
-                                 : "memory");
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    tma_store_2d(&tmO, b, col, row_blk);
-                    bulk_commit();
-                }
-                eb ^= 1u;
-            } else if (valid) {
-                uint4* dst = reinterpret_cast<uint4*>(dst_row);
+            for (int v = 0; v < 4; ++v)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 erow + (((uint32_t)(4 * upper + v) ^ eswz) << 4)),
+                             "r"(pk[4 * v]), "r"(pk[4 * v + 1]), "r"(pk[4 * v + 2]),
+                             "r"(pk[4 * v + 3])
+                             : "memory");
+        };
+        auto put_row = [&](const uint32_t* pk, uint16_t* dst_row) {
+            uint4* dst = reinterpret_cast<uint4*>(dst_row);
 #pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    dst[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+            for (int v = 0; v < 4; ++v)
+                dst[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+        };
+        auto store_tile = [&](int row_blk, int col) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_2d(&tmO, ebuf, col, row_blk);
+                bulk_commit();
             }
         };
         int i = 0;
@@ -449,34 +477,35 @@ __global__ void __launch_bounds__(kXThreads, 1)
             const int row_blk = (int)(ti.row0 + (int64_t)rank * XH + q * 32);
             const bool full_blk = row_blk >= ti.row_beg && (int64_t)row_blk + 31 < ti.row_end;
             if (kGlu) {
-#pragma unroll 1
+                // this warp's 64 columns of h, 32 at a time
+                const int col = ti.n * (XN / 2) + 64 * half;
+                uint32_t codes[8], scales = 0;
+                if (MODE == MX_SWIGLU && full_blk) tile_free();
+#pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const int c = half ? 96 - 32 * k : 32 * k;
+                    const int up = k ^ half;  // half 1 starts with its upper 32 columns
+                    const uint32_t c = (uint32_t)(64 * half + 32 * up);
                     uint32_t g[32], u[32];
-                    if (half) {  // the shared columns first: gates in one half, ups in the other
-                        tmem_ld32(tbase + (uint32_t)(XN / 2 + c), u);
+                    if (half) {  // the shared columns first: ups in this half, gates in the other
+                        tmem_ld32(tbase + (uint32_t)(XN / 2) + c, u);
                         if (k == 0 && over) release_shared();
-                        tmem_ld32(tbase + (uint32_t)c, g);
+                        tmem_ld32(tbase + c, g);
                     } else {
-                        tmem_ld32(tbase + (uint32_t)c, g);
+                        tmem_ld32(tbase + c, g);
                         if (k == 0 && over) release_shared();
-                        tmem_ld32(tbase + (uint32_t)(XN / 2 + c), u);
+                        tmem_ld32(tbase + (uint32_t)(XN / 2) + c, u);
                     }
                     uint32_t pk[16];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float hv[2];
-#pragma unroll
-                        for (int h2 = 0; h2 < 2; ++h2)
-                            hv[h2] = swiglu_fast(__uint_as_float(g[2 * j + h2]),
-                                            __uint_as_float(u[2 * j + h2]));
-                        pk[j] = bf16x2_rne(hv[0], hv[1]);
-                    }
-                    const int col = ti.n * (XN / 2) + c;
+                    for (int j = 0; j < 16; ++j)
+                        pk[j] = bf16x2_rne(swiglu_fast(__uint_as_float(g[2 * j]),
+                                                       __uint_as_float(u[2 * j])),
+                                           swiglu_fast(__uint_as_float(g[2 * j + 1]),
+                                                       __uint_as_float(u[2 * j + 1])));
                     if (MODE == MX_SWIGLU) {
-                        store_block(pk, full_blk, valid, row_blk, col,
-                                    args.out + grow * args.n + col);
-                    } else if (valid) {
+                        if (full_blk) put32(pk, up);
+                        else if (valid) put_row(pk, args.out + grow * args.n + col + 32 * up);
+                    } else {
                         // 32 columns of a row are one block: quantised from the bf16 values, so
                         // the fused product gives the codes of the two calls it replaces
                         uint32_t m = 0;
@@ -484,7 +513,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
                         for (int j = 0; j < 16; ++j)
                             m = max(m, max(pk[j] << 16 & 0x7fffffffu, pk[j] & 0x7fff0000u));
                         const uint32_t s = mx_scale_byte(m);
-                        uint32_t code[4];
+                        scales |= s << (8 * up);
 #pragma unroll
                         for (int v = 0; v < 4; ++v) {
                             float f[8];
@@ -493,27 +522,46 @@ __global__ void __launch_bounds__(kXThreads, 1)
                                 f[2 * e] = __uint_as_float(pk[4 * v + e] << 16);
                                 f[2 * e + 1] = __uint_as_float(pk[4 * v + e] & 0xffff0000u);
                             }
-                            code[v] = mx_encode8(f, s);
+                            const uint32_t w = mx_encode8(f, s);
+                            if (up) codes[4 + v] = w;
+                            else codes[v] = w;
                         }
-                        *reinterpret_cast<uint4*>(args.out_codes + grow * (args.n / 2) + col / 2) =
-                            make_uint4(code[0], code[1], code[2], code[3]);
-                        args.out_scales[mx_tiled_scale(grow, col / 32, args.n / 32)] = (uint8_t)s;
                     }
+                }
+                if (MODE == MX_SWIGLU) {
+                    if (full_blk) store_tile(row_blk, col);
+                } else if (valid) {
+                    uint4* dst = reinterpret_cast<uint4*>(args.out_codes + grow * (args.n / 2) +
+                                                          col / 2);
+                    dst[0] = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+                    dst[1] = make_uint4(codes[4], codes[5], codes[6], codes[7]);
+                    *reinterpret_cast<uint16_t*>(
+                        args.out_scales + mx_tiled_scale(grow, col / 32, args.n / 32)) =
+                        (uint16_t)scales;
                 }
             } else {
 #pragma unroll 1
-                for (int k = 0; k < 4; ++k) {
-                    const int c = half ? 224 - 32 * k : 32 * k;
+                for (int k = 0; k < 2; ++k) {
+                    // each half from its outer end, where the shared columns are
+                    const int c = half ? 192 - 64 * k : 64 * k;
                     const int col = ti.n * XN + c;
-                    uint32_t r[32];
-                    tmem_ld32(tbase + (uint32_t)c, r);
+                    uint32_t r[64];
+                    tmem_ld64(tbase + (uint32_t)c, r);
                     if (k == 0 && over) release_shared();
                     if (col >= args.n) continue;  // past the last column (n a multiple of 128)
-                    uint32_t pk[16];
+                    uint32_t pk[32];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
+                    for (int j = 0; j < 32; ++j)
                         pk[j] = bf16x2_rne(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-                    store_block(pk, full_blk, valid, row_blk, col, args.out + grow * args.n + col);
+                    if (full_blk) {
+                        tile_free();
+                        put32(pk, 0);
+                        put32(pk + 16, 1);
+                        store_tile(row_blk, col);
+                    } else if (valid) {
+                        put_row(pk, args.out + grow * args.n + col);
+                        put_row(pk + 16, args.out + grow * args.n + col + 32);
+                    }
                 }
             }
             tc_fence_before();
@@ -562,6 +610,20 @@ bool make_scale_map(CUtensorMap* m, const void* ptr, int64_t tiles)
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// bf16 [rows, n] as store tiles of 32 rows by 64 columns, 128-byte swizzle
+bool make_out_map(CUtensorMap* m, void* ptr, int64_t rows, int64_t n)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)n, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)n * 2};
+    cuuint32_t box[2] = {64, 32};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int MODE>
 cudaError_t launch_mode(const MxProblem& p, cudaStream_t st)
 {
@@ -590,7 +652,7 @@ cudaError_t launch_mode(const MxProblem& p, cudaStream_t st)
     if (!make_scale_map(&ms, p.b_scales, (int64_t)p.groups * (b_rows / 128) * (p.k / 128)))
         return cudaErrorInvalidValue;
     if (MODE == MX_SWIGLU_QUANT) mo = ma;  // stored from registers: the map is not used
-    else if (!make_store_map(&mo, p.out, p.rows, p.n, p.n)) return cudaErrorInvalidValue;
+    else if (!make_out_map(&mo, p.out, p.rows, p.n)) return cudaErrorInvalidValue;
     MxArgs a{};
     a.k = p.k;
     a.k_blocks = (p.k + XK - 1) / XK;
