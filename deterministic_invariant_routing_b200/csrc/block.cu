@@ -6,7 +6,7 @@
 //
 // n is taken from the rounded r, so the fused call gives the bits of the two calls it replaces.
 // Every sum is fp32 in an order that depends on H alone (a thread's own vectors, a shuffle
-// tree, the warps in order): a token's row never depends on T or on its neighbours.
+// tree in each warp, the same tree over the warps): a token's row never depends on T or on its neighbours.
 //
 // All of it is bound by memory: 4 row passes forward (x, y in; r, n out), 6 backward (y, r, dr,
 // dn in; dx, dy out). A row stays in the registers of one block (one warp up to H = 512), so
@@ -34,21 +34,26 @@ struct NormArgs {
     uint32_t first_row, threshold;
     int32_t gate_mode, param_f32;
     int32_t slot_next, slot_post, slot_gate, slots;  // partial rows of a block, -1: none
-    float eps, residual_scale, branch_scale, inv_keep;
+    float eps, inv_h, residual_scale, branch_scale, inv_keep;  // inv_h: 1 / H
 };
 
-// Sums K values over a row's threads: in order within the shuffle tree, then over the warps in
-// order through shared memory. ROWS > 1 means one warp per row. `red` alternates between two
-// halves, so one barrier a call is enough (a warp that writes a half again has passed the
-// barrier of the call in between, which every reader of that half had reached).
+// Sums K values over a row's threads: a shuffle tree within each warp, then the same tree over
+// the warps' sums, read from shared memory by every warp. `red` alternates between two halves,
+// so one barrier a call is enough (a warp that writes a half again has passed the barrier of
+// the call in between, which every reader of that half had reached).
+template <int K>
+__device__ __forceinline__ void warp_sum(float (&v)[K])
+{
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
+}
+
 template <int K, bool ONEWARP>
 __device__ __forceinline__ void row_sum(float (&v)[K], float* red, int& half)
 {
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1)
-            v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
+    warp_sum<K>(v);
     if (ONEWARP) return;
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float* b = red + half * 32 * K;
@@ -58,16 +63,13 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float* red, int& half)
         for (int k = 0; k < K; ++k) b[k * 32 + warp] = v[k];
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        float s = b[k * 32];
-        for (int w = 1; w < warps; ++w) s += b[k * 32 + w];
-        v[k] = s;
-    }
+    for (int k = 0; k < K; ++k) v[k] = lane < warps ? b[k * 32 + lane] : 0.0f;
+    warp_sum<K>(v);
 }
 
 __device__ __forceinline__ float inv_rms(float ss, const NormArgs& a)
 {
-    return 1.0f / sqrtf(ss / (float)a.H + a.eps);
+    return rsqrtf(ss * a.inv_h + a.eps);
 }
 
 __device__ __forceinline__ uint32_t row_id(const NormArgs& a, int64_t t)
@@ -200,40 +202,100 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT) residual_norm_kernel(
 //   dgate = b z (summed over tokens, over columns, or kept),  c = drop'(b gate)
 //   dy = u w_post c - y u^3 mean(w_post c y)             u = 1 / sqrt(mean(y^2) + eps)
 //   dw_next = sum_t dn r s,  dw_post = sum_t c y u
+//
+// A thread's three accumulators for each of its columns take most of its registers, so few
+// warps fit on an SM and loads have to be in flight without them: each thread copies its own
+// vectors of the next rows to its own slots of a ring in shared memory (cp.async; nobody else
+// reads them, so no barrier) and reads them back, twice, when their row comes. Rows too wide
+// for a stage of the ring (fp32 above H = 8192) are read from memory instead.
+struct BwdRing {
+    int32_t stages, arrays;               // stages 0: no ring
+    int32_t i_r, i_dn, i_dr, i_y, i_gate; // place of each array in a stage, -1: absent
+};
+
 template <int DT, int V, int MAXT>
-__global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT) residual_norm_bwd_kernel(NormArgs a)
+__global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32 || MAXT == 128 ? 4
+                                                           : MAXT == 256              ? 2
+                                                                                      : 1)
+    residual_norm_bwd_kernel(NormArgs a, BwdRing g)
 {
     constexpr bool ONEWARP = MAXT == 32;
+    constexpr int W16 = DT == MOE_F32 ? 2 : 1;  // 16-byte words of a vector
+    extern __shared__ uint4 ring[];
     __shared__ float red[2 * 32 * 3];
     int half = 0;
     pdl_wait();
     const int tid = threadIdx.x, step = blockDim.x;
+    const int lin = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
     const int64_t rows = ONEWARP ? (int64_t)gridDim.x * blockDim.y : gridDim.x;
     const int64_t first = ONEWARP ? (int64_t)blockIdx.x * blockDim.y + threadIdx.y : blockIdx.x;
     const bool post = a.w_post != nullptr, next = a.w_next != nullptr, branch = a.y != nullptr;
+    const bool drop = a.threshold != 0;
     float gn[V][8], gp[V][8], gg[V][8];
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) gn[i][e] = gp[i][e] = gg[i][e] = 0.0f;
     Philox ph;
-    if (a.threshold) ph = philox_load(a.rng);
+    if (drop) ph = philox_load(a.rng);
+
+    auto slot = [&](int stage, int array, int i) {
+        return ring + ((int64_t)(stage * g.arrays + array) * (V * W16) + i * W16) * threads + lin;
+    };
+    auto fetch = [&](int stage, int64_t t) {
+        auto one = [&](int array, const void* p) {
+            if (array < 0) return;
+            const uint4* src = static_cast<const uint4*>(p) + t * a.nvec * W16;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int v = tid + i * step;
+                if (v < a.nvec) {
+                    uint4* dst = slot(stage, array, i);
+#pragma unroll
+                    for (int h = 0; h < W16; ++h)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                         (uint32_t)__cvta_generic_to_shared(dst + h * threads)),
+                                     "l"(src + v * W16 + h)
+                                     : "memory");
+                }
+            }
+        };
+        if (t < a.T) {
+            one(g.i_r, a.r);
+            one(g.i_dn, a.dn);
+            one(g.i_dr, a.dr);
+            one(g.i_y, a.y);
+            one(g.i_gate, a.gate);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto row_ready = [&]() {  // at most stages - 1 newer rows still in flight
+        switch (g.stages) {
+            case 1: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+            case 2: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+            case 3: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+            default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+        }
+    };
+    int stage = 0;
+    auto get = [&](int array, const void* p, int64_t row, int i, float (&f)[8]) {
+        Vec8<DT> q;
+        if (g.stages > 0) {
+            const uint4* src = slot(stage, array, i);
+            uint4 w[W16];
+#pragma unroll
+            for (int h = 0; h < W16; ++h) w[h] = src[h * threads];
+            q.load(w, 0);
+        } else {
+            q.load(p, row + tid + i * step);
+        }
+        q.get(f);
+    };
+    for (int s = 0; s < g.stages; ++s) fetch(s, first + s * rows);
 
     for (int64_t t = first; t < a.T; t += rows) {
         const int64_t row = t * a.nvec;
-        Vec8<DT> r[V], y[V], dn[V], dr[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int v = tid + i * step;
-            if (v < a.nvec) {
-                if (next) {
-                    r[i].load(a.r, row + v);
-                    dn[i].load(a.dn, row + v);
-                }
-                if (a.dr != nullptr) dr[i].load(a.dr, row + v);
-                if (branch) y[i].load(a.y, row + v);
-            }
-        }
+        if (g.stages > 0) row_ready();
         float s3[3] = {0.0f, 0.0f, 0.0f};  // r^2, w_next dn r, y^2
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -241,8 +303,8 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT) residual_norm_bwd_ker
             if (v < a.nvec) {
                 if (next) {
                     float p[8], q[8], w[8];
-                    r[i].get(p);
-                    dn[i].get(q);
+                    get(g.i_r, a.r, row, i, p);
+                    get(g.i_dn, a.dn, row, i, q);
                     load_param8<DT>(a.w_next, a.param_f32, v, w);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -252,19 +314,19 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT) residual_norm_bwd_ker
                 }
                 if (post) {
                     float p[8];
-                    y[i].get(p);
+                    get(g.i_y, a.y, row, i, p);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) s3[2] = fmaf(p[e], p[e], s3[2]);
                 }
             }
         }
-        row_sum<3, ONEWARP>(s3, red, half);
+        if (next || post) row_sum<3, ONEWARP>(s3, red, half);
         const float s = next ? inv_rms(s3[0], a) : 0.0f;
-        const float mean_n = next ? s * s * (s3[1] / (float)a.H) : 0.0f;
+        const float mean_n = next ? s * s * (s3[1] * a.inv_h) : 0.0f;
         const float u = post ? inv_rms(s3[2], a) : 1.0f;
         const float tg = a.gate_mode == MOE_GATE_TOKEN ? load_param<DT>(a.gate, a.param_f32, t)
                                                        : 1.0f;
-        const uint32_t rid = row_id(a, t);
+        const uint32_t rid = drop ? row_id(a, t) : 0u;
         float s2[2] = {0.0f, 0.0f};  // w_post c y, b z
         float c[V][8];
 #pragma unroll
@@ -273,15 +335,15 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT) residual_norm_bwd_ker
             if (v < a.nvec) {
                 float d[8], q[8];
                 if (a.dr != nullptr) {
-                    dr[i].get(d);
+                    get(g.i_dr, a.dr, row, i, d);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) d[e] = 0.0f;
                 }
                 if (next) {
                     float p[8], w[8];
-                    r[i].get(p);
-                    dn[i].get(q);
+                    get(g.i_r, a.r, row, i, p);
+                    get(g.i_dn, a.dn, row, i, q);
                     load_param8<DT>(a.w_next, a.param_f32, v, w);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -295,53 +357,56 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT) residual_norm_bwd_ker
                 o.set(q);
                 o.store(a.dx, row + v);
                 if (branch) {
-                    float yv[8], w[8];
-                    uint32_t bitsw[4] = {0u, 0u, 0u, 0u};
-                    if (a.threshold) philox8(ph, (uint32_t)v, rid, bitsw);
-                    y[i].get(yv);
+                    float y[8], w[8];
+                    uint32_t bitsw[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+                    if (drop) philox8(ph, (uint32_t)v, rid, bitsw);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) d[e] *= a.branch_scale;
+                    get(g.i_y, a.y, row, i, y);
                     if (post) load_param8<DT>(a.w_post, a.param_f32, v, w);
                     if (a.gate_mode != MOE_GATE_NONE) {
                         float z[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            z[e] = post ? yv[e] * u * w[e] : yv[e];
-                            if (a.threshold)
-                                z[e] = philox_keep(bitsw, e, a.threshold) ? z[e] * a.inv_keep
-                                                                          : 0.0f;
+                        for (int e = 0; e < 8; ++e) z[e] = post ? y[e] * u * w[e] : y[e];
+                        if (drop) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                z[e] = philox_keep(bitsw, e, a.threshold) ? z[e] * a.inv_keep : 0.0f;
                         }
-                        gate8<DT>(a, t, v, tg, q);
                         if (a.gate_mode == MOE_GATE_FULL) {
+                            get(g.i_gate, a.gate, row, i, q);
 #pragma unroll
                             for (int e = 0; e < 8; ++e) z[e] *= d[e];
                             o.set(z);
                             o.store(a.dgate, row + v);
                         } else if (a.gate_mode == MOE_GATE_CHANNEL) {
+                            load_param8<DT>(a.gate, a.param_f32, v, q);
 #pragma unroll
                             for (int e = 0; e < 8; ++e) gg[i][e] = fmaf(d[e], z[e], gg[i][e]);
                         } else {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) s2[1] = fmaf(d[e], z[e], s2[1]);
+                            for (int e = 0; e < 8; ++e) {
+                                s2[1] = fmaf(d[e], z[e], s2[1]);
+                                q[e] = tg;
+                            }
                         }
 #pragma unroll
                         for (int e = 0; e < 8; ++e) d[e] *= q[e];
                     }
+                    if (drop) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        c[i][e] = d[e];
-                        if (a.threshold)
-                            c[i][e] = philox_keep(bitsw, e, a.threshold) ? d[e] * a.inv_keep : 0.0f;
+                        for (int e = 0; e < 8; ++e)
+                            d[e] = philox_keep(bitsw, e, a.threshold) ? d[e] * a.inv_keep : 0.0f;
                     }
                     if (post) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            gp[i][e] = fmaf(c[i][e], yv[e] * u, gp[i][e]);
-                            c[i][e] *= w[e];
-                            s2[0] = fmaf(c[i][e], yv[e], s2[0]);
+                            gp[i][e] = fmaf(d[e], y[e] * u, gp[i][e]);
+                            c[i][e] = d[e] * w[e];
+                            s2[0] = fmaf(c[i][e], y[e], s2[0]);
                         }
                     } else {
-                        o.set(c[i]);
+                        o.set(d);
                         o.store(a.dy, row + v);
                     }
                 }
@@ -350,34 +415,38 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT) residual_norm_bwd_ker
         if (post || a.gate_mode == MOE_GATE_TOKEN) row_sum<2, ONEWARP>(s2, red, half);
         if (a.gate_mode == MOE_GATE_TOKEN && tid == 0) static_cast<float*>(a.dgate)[t] = s2[1];
         if (post) {
-            const float mean_p = u * u * (s2[0] / (float)a.H);
+            const float mean_p = u * u * (s2[0] * a.inv_h);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int v = tid + i * step;
                 if (v < a.nvec) {
-                    float yv[8];
-                    y[i].get(yv);
+                    float y[8];
+                    get(g.i_y, a.y, row, i, y);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) yv[e] = u * (c[i][e] - yv[e] * mean_p);
+                    for (int e = 0; e < 8; ++e) y[e] = u * (c[i][e] - y[e] * mean_p);
                     Vec8<DT> o;
-                    o.set(yv);
+                    o.set(y);
                     o.store(a.dy, row + v);
                 }
             }
+        }
+        if (g.stages > 0) {
+            fetch(stage, t + g.stages * rows);
+            if (++stage == g.stages) stage = 0;
         }
     }
 
     // this row group's partial sums
     float* part = a.part + first * a.slots * (int64_t)a.H;
-    auto put = [&](int slot, const float (&g)[V][8]) {
-        if (slot < 0) return;
+    auto put = [&](int where, const float (&f)[V][8]) {
+        if (where < 0) return;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int v = tid + i * step;
             if (v < a.nvec) {
-                float4* d = reinterpret_cast<float4*>(part + (int64_t)slot * a.H) + 2 * v;
-                d[0] = make_float4(g[i][0], g[i][1], g[i][2], g[i][3]);
-                d[1] = make_float4(g[i][4], g[i][5], g[i][6], g[i][7]);
+                float4* d = reinterpret_cast<float4*>(part + (int64_t)where * a.H) + 2 * v;
+                d[0] = make_float4(f[i][0], f[i][1], f[i][2], f[i][3]);
+                d[1] = make_float4(f[i][4], f[i][5], f[i][6], f[i][7]);
             }
         }
     };
@@ -387,18 +456,19 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT) residual_norm_bwd_ker
 }
 
 // out[slot][column] = sum over the partial rows in order: a warp takes 32 columns of a slice of
-// the rows, the 8 slices of a block are added in order
+// the rows, the slices of a block are added in order. Bound by the latency of a slice's loads,
+// hence many short slices.
 struct ReduceArgs {
     const float* part;
     int32_t parts, slots, H;
     float* out[3];
 };
 
-constexpr int kSlices = 8;
+constexpr int kSlices = 32;
 
 __global__ void __launch_bounds__(32 * kSlices) param_grad_kernel(ReduceArgs a)
 {
-    __shared__ float red[kSlices][32];
+    __shared__ float red[kSlices][33];
     pdl_wait();
     const int lane = threadIdx.x, slice = threadIdx.y;
     const int col = blockIdx.x * 32 + lane, slot = blockIdx.y;
@@ -415,6 +485,7 @@ __global__ void __launch_bounds__(32 * kSlices) param_grad_kernel(ReduceArgs a)
     __syncthreads();
     if (slice == 0 && col < a.H) {
         s = red[0][lane];
+#pragma unroll
         for (int i = 1; i < kSlices; ++i) s += red[i][lane];
         a.out[slot][col] = s;
     }
@@ -473,15 +544,24 @@ RowShape row_shape(int nvec)
 
 constexpr int kWarpRows = 4;  // rows of a block in the one-warp form
 
+// the backward keeps 24 sums per vector in registers: one vector a thread up to H = 4096
+RowShape bwd_shape(int nvec)
+{
+    if (nvec <= 32) return {true, 1, 32};
+    if (nvec <= 512) return {false, 1, (nvec + 31) / 32 * 32};
+    return {false, 2, ((nvec + 1) / 2 + 31) / 32 * 32};
+}
+
 // row groups of the backward: a function of (T, H) alone, so that the order of the parameter
-// sums does not depend on the device (about 512 threads for each of a B200's 148 SMs)
+// sums does not depend on the device (about 512 threads for each of a B200's 148 SMs, at least
+// two rows a group)
 int64_t bwd_groups(int64_t T, int32_t H)
 {
-    const RowShape s = row_shape(H / 8);
+    const RowShape s = bwd_shape(H / 8);
     int64_t per_sm = 512 / s.threads;
     if (per_sm < 1) per_sm = 1;
     int64_t g = 148 * per_sm;
-    if (g > T) g = T;
+    if (g > (T + 1) / 2) g = (T + 1) / 2;
     if (s.one_warp) g = (g + kWarpRows - 1) / kWarpRows * kWarpRows;
     return g;
 }
@@ -498,6 +578,7 @@ NormArgs base_args(const moe_norm_cfg& c)
     a.gate_mode = c.gate;
     a.param_f32 = c.param_dtype == MOE_F32;
     a.eps = c.eps;
+    a.inv_h = 1.0f / (float)c.H;
     a.residual_scale = c.residual_scale;
     a.branch_scale = c.branch_scale;
     return a;
@@ -518,19 +599,51 @@ cudaError_t norm_fwd(const NormArgs& a, cudaStream_t st)
     return launch_pdl(kernel, dim3((unsigned)a.T), dim3(s.threads), 0, st, a);
 }
 
+template <int DT, int V, int MAXT>
+cudaError_t norm_bwd_variant(const NormArgs& a, BwdRing g, dim3 grid, dim3 block, cudaStream_t st)
+{
+    auto kernel = residual_norm_bwd_kernel<DT, V, MAXT>;
+    const int threads = (int)(block.x * block.y);
+    const int per_sm = threads <= 512 ? 512 / threads : 1;
+    const size_t stage = (size_t)g.arrays * V * (DT == MOE_F32 ? 32 : 16) * threads;
+    g.stages = (int32_t)(225000 / per_sm / (stage > 0 ? stage : 1));
+    if (g.stages > 4) g.stages = 4;
+    const size_t smem = g.stages * stage;
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    static bool attr_set[64] = {};
+    if (!attr_set[dev]) {
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 226000);
+        if (err != cudaSuccess) return err;
+        attr_set[dev] = true;
+    }
+    return launch_pdl(kernel, grid, block, smem, st, a, g);
+}
+
 template <int DT>
 cudaError_t norm_bwd(const NormArgs& a, int64_t groups, cudaStream_t st)
 {
-    const RowShape s = row_shape(a.nvec);
-    if (s.one_warp) {
-        const dim3 grid((unsigned)(groups / kWarpRows)), block(32, kWarpRows);
-        return s.V == 1 ? launch_pdl(residual_norm_bwd_kernel<DT, 1, 32>, grid, block, 0, st, a)
-                        : launch_pdl(residual_norm_bwd_kernel<DT, 2, 32>, grid, block, 0, st, a);
+    BwdRing g{};
+    auto take = [&](bool on) { return on ? g.arrays++ : -1; };
+    g.i_r = take(a.w_next != nullptr);
+    g.i_dn = take(a.w_next != nullptr);
+    g.i_dr = take(a.dr != nullptr);
+    g.i_y = take(a.y != nullptr);
+    g.i_gate = take(a.gate_mode == MOE_GATE_FULL);
+    const RowShape s = bwd_shape(a.nvec);
+    if (s.one_warp)
+        return norm_bwd_variant<DT, 1, 32>(a, g, dim3((unsigned)(groups / kWarpRows)),
+                                           dim3(32, kWarpRows), st);
+    const dim3 grid((unsigned)groups), block(s.threads);
+    if (s.V == 1) {
+        if (s.threads <= 128) return norm_bwd_variant<DT, 1, 128>(a, g, grid, block, st);
+        if (s.threads <= 256) return norm_bwd_variant<DT, 1, 256>(a, g, grid, block, st);
+        return norm_bwd_variant<DT, 1, 512>(a, g, grid, block, st);
     }
-    auto kernel = s.threads <= 256   ? residual_norm_bwd_kernel<DT, 2, 256>
-                  : s.threads <= 512 ? residual_norm_bwd_kernel<DT, 2, 512>
-                                     : residual_norm_bwd_kernel<DT, 2, 1024>;
-    return launch_pdl(kernel, dim3((unsigned)groups), dim3(s.threads), 0, st, a);
+    if (s.threads <= 512) return norm_bwd_variant<DT, 2, 512>(a, g, grid, block, st);
+    return norm_bwd_variant<DT, 2, 1024>(a, g, grid, block, st);
 }
 
 int bwd_slots(const moe_norm_cfg& c, bool post, bool next)
