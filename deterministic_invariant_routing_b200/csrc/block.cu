@@ -77,20 +77,15 @@ __device__ __forceinline__ uint32_t row_id(const NormArgs& a, int64_t t)
     return a.row_ids != nullptr ? (uint32_t)a.row_ids[t] : a.first_row + (uint32_t)t;
 }
 
-// a gate's 8 values for one vector of row t
-template <int DT>
-__device__ __forceinline__ void gate8(const NormArgs& a, int64_t t, int v, float token_gate,
-                                      float (&g)[8])
+// the kept elements of a vector, 0 elsewhere (a select: dropped infinities and NaNs give 0)
+__device__ __forceinline__ void drop2(const uint32_t (&w)[4], uint32_t threshold, F2 (&f)[4])
 {
-    if (a.gate_mode == MOE_GATE_CHANNEL) {
-        load_param8<DT>(a.gate, a.param_f32, v, g);
-    } else if (a.gate_mode == MOE_GATE_FULL) {
-        Vec8<DT> q;
-        q.load(a.gate, t * a.nvec + v);
-        q.get(g);
-    } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = token_gate;
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        unpack(f[i], lo, hi);
+        f[i] = f2(philox_keep(w, 2 * i, threshold) ? lo : 0.0f,
+                  philox_keep(w, 2 * i + 1, threshold) ? hi : 0.0f);
     }
 }
 
@@ -115,83 +110,90 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT) residual_norm_kernel(
             if (a.y != nullptr) y[i].load(a.y, row + v);
         }
     }
-    float f[V][8];
     if (a.y != nullptr) {
-        float inv = 1.0f;
+        float scale = a.branch_scale * (a.threshold ? a.inv_keep : 1.0f);
         if (a.w_post != nullptr) {
-            float ss[1] = {0.0f};
+            F2 acc = f2(0.0f);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 if (tid + i * step < a.nvec) {
-                    float q[8];
-                    y[i].get(q);
+                    F2 q[4];
+                    get2(y[i], q);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) ss[0] = fmaf(q[e], q[e], ss[0]);
+                    for (int e = 0; e < 4; ++e) acc = fma2(q[e], q[e], acc);
                 }
             }
+            float ss[1] = {sum2(acc)};
             row_sum<1, ONEWARP>(ss, red, half);
-            inv = inv_rms(ss[0], a);
+            scale *= inv_rms(ss[0], a);
         }
-        const float tg = a.gate_mode == MOE_GATE_TOKEN ? load_param<DT>(a.gate, a.param_f32, t)
-                                                       : 1.0f;
+        if (a.gate_mode == MOE_GATE_TOKEN) scale *= load_param<DT>(a.gate, a.param_f32, t);
         Philox ph;
         if (a.threshold) ph = philox_load(a.rng);
-        const uint32_t rid = row_id(a, t);
+        const uint32_t rid = a.threshold ? row_id(a, t) : 0u;
+        const F2 sc = f2(scale), rs = f2(a.residual_scale);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int v = tid + i * step;
             if (v < a.nvec) {
-                float z[8], q[8];
-                y[i].get(z);
-                if (a.w_post != nullptr) {
-                    load_param8<DT>(a.w_post, a.param_f32, v, q);
+                F2 z[4], q[4];
+                get2(y[i], z);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) z[e] = z[e] * inv * q[e];
+                for (int e = 0; e < 4; ++e) z[e] = mul2(z[e], sc);
+                if (a.w_post != nullptr) {
+                    load_param2<DT>(a.w_post, a.param_f32, v, q);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[e] = mul2(z[e], q[e]);
                 }
                 if (a.threshold) {
                     uint32_t w[4];
                     philox8(ph, (uint32_t)v, rid, w);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        z[e] = philox_keep(w, e, a.threshold) ? z[e] * a.inv_keep : 0.0f;
+                    drop2(w, a.threshold, z);
                 }
-                if (a.gate_mode != MOE_GATE_NONE) {
-                    gate8<DT>(a, t, v, tg, q);
+                if (a.gate_mode >= MOE_GATE_CHANNEL && a.gate_mode != MOE_GATE_TOKEN) {
+                    if (a.gate_mode == MOE_GATE_CHANNEL) {
+                        load_param2<DT>(a.gate, a.param_f32, v, q);
+                    } else {
+                        Vec8<DT> g;
+                        g.load(a.gate, row + v);
+                        get2(g, q);
+                    }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) z[e] *= q[e];
+                    for (int e = 0; e < 4; ++e) z[e] = mul2(z[e], q[e]);
                 }
-                x[i].get(q);
+                get2(x[i], q);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    q[e] = a.residual_scale * q[e] + a.branch_scale * z[e];
-                x[i].set(q);
+                for (int e = 0; e < 4; ++e) q[e] = fma2(rs, q[e], z[e]);
+                set2(x[i], q);
                 x[i].store(a.r, row + v);
             }
         }
     }
     if (a.w_next == nullptr) return;
-    float ss[1] = {0.0f};
+    F2 acc = f2(0.0f);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         if (tid + i * step < a.nvec) {
-            x[i].get(f[i]);  // the rounded r
+            F2 q[4];
+            get2(x[i], q);  // the rounded r
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss[0] = fmaf(f[i][e], f[i][e], ss[0]);
+            for (int e = 0; e < 4; ++e) acc = fma2(q[e], q[e], acc);
         }
     }
+    float ss[1] = {sum2(acc)};
     row_sum<1, ONEWARP>(ss, red, half);
-    const float inv = inv_rms(ss[0], a);
+    const F2 inv = f2(inv_rms(ss[0], a));
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int v = tid + i * step;
         if (v < a.nvec) {
-            float q[8];
-            load_param8<DT>(a.w_next, a.param_f32, v, q);
+            F2 q[4], w[4];
+            get2(x[i], q);
+            load_param2<DT>(a.w_next, a.param_f32, v, w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) q[e] = f[i][e] * inv * q[e];
-            Vec8<DT> o;
-            o.set(q);
-            o.store(a.n, row + v);
+            for (int e = 0; e < 4; ++e) q[e] = mul2(mul2(q[e], inv), w[e]);
+            set2(x[i], q);
+            x[i].store(a.n, row + v);
         }
     }
 }
@@ -213,13 +215,18 @@ struct BwdRing {
     int32_t i_r, i_dn, i_dr, i_y, i_gate; // place of each array in a stage, -1: absent
 };
 
-template <int DT, int V, int MAXT>
-__global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32 || MAXT == 128 ? 4
-                                                           : MAXT == 256              ? 2
-                                                                                      : 1)
-    residual_norm_bwd_kernel(NormArgs a, BwdRing g)
+// MODE: kBwdAny looks at what is present as it goes; kBwdAll and kBwdAllDrop are the usual call,
+// with both norms, dr, fp32 parameters and room for the ring, without and with dropout. Bound by
+// instructions, the looking costs: of 100 per element a fifth were branches and their constants.
+enum { kBwdAny = 0, kBwdAll = 1, kBwdAllDrop = 2 };
+
+template <int DT, int V, int MAXT, int MODE>
+__global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
+                                                           : MAXT == 256 ? 2
+                                                                         : 1)
+    residual_norm_bwd_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ BwdRing g)
 {
-    constexpr bool ONEWARP = MAXT == 32;
+    constexpr bool ONEWARP = MAXT == 32, ALL = MODE != kBwdAny;
     constexpr int W16 = DT == MOE_F32 ? 2 : 1;  // 16-byte words of a vector
     extern __shared__ uint4 ring[];
     __shared__ float red[2 * 32 * 3];
@@ -229,42 +236,49 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32 || MAXT ==
     const int lin = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
     const int64_t rows = ONEWARP ? (int64_t)gridDim.x * blockDim.y : gridDim.x;
     const int64_t first = ONEWARP ? (int64_t)blockIdx.x * blockDim.y + threadIdx.y : blockIdx.x;
-    const bool post = a.w_post != nullptr, next = a.w_next != nullptr, branch = a.y != nullptr;
-    const bool drop = a.threshold != 0;
-    float gn[V][8], gp[V][8], gg[V][8];
+    const bool post = ALL || a.w_post != nullptr, next = ALL || a.w_next != nullptr;
+    const bool branch = ALL || a.y != nullptr, has_dr = ALL || a.dr != nullptr;
+    const bool drop = MODE == kBwdAllDrop || (MODE == kBwdAny && a.threshold != 0);
+    const bool has_ring = ALL || g.stages > 0, param_f32 = ALL || a.param_f32;
+    const int nvec = a.nvec, gate_mode = a.gate_mode;
+    const uint32_t threshold = a.threshold;
+    // places of the arrays in a stage
+    const int at_r = ALL ? 0 : g.i_r, at_dn = ALL ? 1 : g.i_dn, at_dr = ALL ? 2 : g.i_dr,
+              at_y = ALL ? 3 : g.i_y;
+    F2 gn[V][4], gp[V][4], gg[V][4];
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) gn[i][e] = gp[i][e] = gg[i][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) gn[i][e] = gp[i][e] = gg[i][e] = f2(0.0f);
     Philox ph;
     if (drop) ph = philox_load(a.rng);
 
-    auto slot = [&](int stage, int array, int i) {
-        return ring + ((int64_t)(stage * g.arrays + array) * (V * W16) + i * W16) * threads + lin;
-    };
-    auto fetch = [&](int stage, int64_t t) {
+    // this thread's place in the ring: 16 bytes per thread, arrays and vectors `lane16` apart
+    const uint32_t lane16 = (uint32_t)threads * 16u;
+    const uint32_t ring0 = (uint32_t)__cvta_generic_to_shared(ring) + (uint32_t)lin * 16u;
+    const uint32_t stage_bytes = (uint32_t)(g.arrays * V * W16) * lane16;
+    auto fetch = [&](uint32_t at, int64_t t) {
         auto one = [&](int array, const void* p) {
             if (array < 0) return;
-            const uint4* src = static_cast<const uint4*>(p) + t * a.nvec * W16;
+            const uint4* src = static_cast<const uint4*>(p) + t * nvec * W16;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int v = tid + i * step;
-                if (v < a.nvec) {
-                    uint4* dst = slot(stage, array, i);
+                if (v < nvec) {
 #pragma unroll
                     for (int h = 0; h < W16; ++h)
                         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                         (uint32_t)__cvta_generic_to_shared(dst + h * threads)),
+                                         at + (uint32_t)((array * V + i) * W16 + h) * lane16),
                                      "l"(src + v * W16 + h)
                                      : "memory");
                 }
             }
         };
         if (t < a.T) {
-            one(g.i_r, a.r);
-            one(g.i_dn, a.dn);
-            one(g.i_dr, a.dr);
-            one(g.i_y, a.y);
+            one(at_r, a.r);
+            one(at_dn, a.dn);
+            one(at_dr, a.dr);
+            one(at_y, a.y);
             one(g.i_gate, a.gate);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -277,176 +291,185 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32 || MAXT ==
             default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
         }
     };
-    int stage = 0;
-    auto get = [&](int array, const void* p, int64_t row, int i, float (&f)[8]) {
+    uint32_t at = ring0;  // the current row's stage
+    auto get = [&](int array, const void* p, int64_t row, int i, F2 (&f)[4]) {
         Vec8<DT> q;
-        if (g.stages > 0) {
-            const uint4* src = slot(stage, array, i);
+        if (has_ring) {
             uint4 w[W16];
 #pragma unroll
-            for (int h = 0; h < W16; ++h) w[h] = src[h * threads];
+            for (int h = 0; h < W16; ++h)
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[h].x), "=r"(w[h].y), "=r"(w[h].z), "=r"(w[h].w)
+                             : "r"(at + (uint32_t)((array * V + i) * W16 + h) * lane16)
+                             : "memory");
             q.load(w, 0);
         } else {
             q.load(p, row + tid + i * step);
         }
-        q.get(f);
+        get2(q, f);
     };
-    for (int s = 0; s < g.stages; ++s) fetch(s, first + s * rows);
+    for (int s = 0; s < g.stages; ++s) fetch(ring0 + (uint32_t)s * stage_bytes, first + s * rows);
 
+    const F2 rscale = f2(a.residual_scale);
+    const F2 bscale = f2(a.branch_scale * (drop ? a.inv_keep : 1.0f));  // with 1 / P(keep)
     for (int64_t t = first; t < a.T; t += rows) {
-        const int64_t row = t * a.nvec;
-        if (g.stages > 0) row_ready();
-        float s3[3] = {0.0f, 0.0f, 0.0f};  // r^2, w_next dn r, y^2
+        const int64_t row = t * nvec;
+        if (has_ring) row_ready();
+        F2 rr = f2(0.0f), wr = f2(0.0f), yy = f2(0.0f);  // r^2, w_next dn r, y^2
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int v = tid + i * step;
-            if (v < a.nvec) {
+            if (v < nvec) {
+                F2 p[4], q[4], w[4];
                 if (next) {
-                    float p[8], q[8], w[8];
-                    get(g.i_r, a.r, row, i, p);
-                    get(g.i_dn, a.dn, row, i, q);
-                    load_param8<DT>(a.w_next, a.param_f32, v, w);
+                    get(at_r, a.r, row, i, p);
+                    get(at_dn, a.dn, row, i, q);
+                    load_param2<DT>(a.w_next, param_f32, v, w);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        s3[0] = fmaf(p[e], p[e], s3[0]);
-                        s3[1] = fmaf(q[e] * w[e], p[e], s3[1]);
+                    for (int e = 0; e < 4; ++e) {
+                        rr = fma2(p[e], p[e], rr);
+                        wr = fma2(mul2(q[e], w[e]), p[e], wr);
                     }
                 }
                 if (post) {
-                    float p[8];
-                    get(g.i_y, a.y, row, i, p);
+                    get(at_y, a.y, row, i, p);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) s3[2] = fmaf(p[e], p[e], s3[2]);
+                    for (int e = 0; e < 4; ++e) yy = fma2(p[e], p[e], yy);
                 }
             }
         }
+        float s3[3] = {sum2(rr), sum2(wr), sum2(yy)};
         if (next || post) row_sum<3, ONEWARP>(s3, red, half);
         const float s = next ? inv_rms(s3[0], a) : 0.0f;
-        const float mean_n = next ? s * s * (s3[1] * a.inv_h) : 0.0f;
+        const F2 s2x = f2(s), mean_n = f2(next ? -s * s * s * (s3[1] * a.inv_h) : 0.0f);
         const float u = post ? inv_rms(s3[2], a) : 1.0f;
-        const float tg = a.gate_mode == MOE_GATE_TOKEN ? load_param<DT>(a.gate, a.param_f32, t)
-                                                       : 1.0f;
+        const F2 u2x = f2(u);
+        const F2 tg = f2(gate_mode == MOE_GATE_TOKEN ? load_param<DT>(a.gate, param_f32, t)
+                                                       : 1.0f);
         const uint32_t rid = drop ? row_id(a, t) : 0u;
-        float s2[2] = {0.0f, 0.0f};  // w_post c y, b z
-        float c[V][8];
+        F2 cy = f2(0.0f), bz = f2(0.0f);  // w_post c y, b z
+        F2 c[V][4];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int v = tid + i * step;
-            if (v < a.nvec) {
-                float d[8], q[8];
-                if (a.dr != nullptr) {
-                    get(g.i_dr, a.dr, row, i, d);
+            if (v < nvec) {
+                F2 d[4], q[4];
+                if (has_dr) {
+                    get(at_dr, a.dr, row, i, d);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) d[e] = 0.0f;
+                    for (int e = 0; e < 4; ++e) d[e] = f2(0.0f);
                 }
                 if (next) {
-                    float p[8], w[8];
-                    get(g.i_r, a.r, row, i, p);
-                    get(g.i_dn, a.dn, row, i, q);
-                    load_param8<DT>(a.w_next, a.param_f32, v, w);
+                    F2 p[4], w[4];
+                    get(at_r, a.r, row, i, p);
+                    get(at_dn, a.dn, row, i, q);
+                    load_param2<DT>(a.w_next, param_f32, v, w);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        d[e] += s * (q[e] * w[e] - p[e] * mean_n);
-                        gn[i][e] = fmaf(q[e], p[e] * s, gn[i][e]);
+                    for (int e = 0; e < 4; ++e) {
+                        const F2 k = mul2(q[e], s2x);
+                        d[e] = fma2(k, w[e], d[e]);
+                        d[e] = fma2(p[e], mean_n, d[e]);
+                        gn[i][e] = fma2(k, p[e], gn[i][e]);
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) q[e] = a.residual_scale * d[e];
+                for (int e = 0; e < 4; ++e) q[e] = mul2(rscale, d[e]);
                 Vec8<DT> o;
-                o.set(q);
+                set2(o, q);
                 o.store(a.dx, row + v);
                 if (branch) {
-                    float y[8], w[8];
-                    uint32_t bitsw[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+                    F2 yu[4], w[4];
+                    uint32_t bitsw[4] = {0u, 0u, 0u, 0u};
                     if (drop) philox8(ph, (uint32_t)v, rid, bitsw);
+                    get(at_y, a.y, row, i, yu);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) d[e] *= a.branch_scale;
-                    get(g.i_y, a.y, row, i, y);
-                    if (post) load_param8<DT>(a.w_post, a.param_f32, v, w);
-                    if (a.gate_mode != MOE_GATE_NONE) {
-                        float z[8];
+                    for (int e = 0; e < 4; ++e) {
+                        d[e] = mul2(d[e], bscale);
+                        yu[e] = mul2(yu[e], u2x);
+                    }
+                    if (post) load_param2<DT>(a.w_post, param_f32, v, w);
+                    if (drop) drop2(bitsw, threshold, d);
+                    if (gate_mode != MOE_GATE_NONE) {
+                        // b z: the factor 1 / P(keep) of z is already in d, dropped ones are 0
+                        F2 z[4];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) z[e] = post ? y[e] * u * w[e] : y[e];
-                        if (drop) {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                z[e] = philox_keep(bitsw, e, a.threshold) ? z[e] * a.inv_keep : 0.0f;
-                        }
-                        if (a.gate_mode == MOE_GATE_FULL) {
+                        for (int e = 0; e < 4; ++e) z[e] = post ? mul2(yu[e], w[e]) : yu[e];
+                        if (drop) drop2(bitsw, threshold, z);
+                        if (gate_mode == MOE_GATE_FULL) {
                             get(g.i_gate, a.gate, row, i, q);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) z[e] *= d[e];
-                            o.set(z);
+                            for (int e = 0; e < 4; ++e) z[e] = mul2(z[e], d[e]);
+                            set2(o, z);
                             o.store(a.dgate, row + v);
-                        } else if (a.gate_mode == MOE_GATE_CHANNEL) {
-                            load_param8<DT>(a.gate, a.param_f32, v, q);
+                        } else if (gate_mode == MOE_GATE_CHANNEL) {
+                            load_param2<DT>(a.gate, param_f32, v, q);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) gg[i][e] = fmaf(d[e], z[e], gg[i][e]);
+                            for (int e = 0; e < 4; ++e) gg[i][e] = fma2(d[e], z[e], gg[i][e]);
                         } else {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                s2[1] = fmaf(d[e], z[e], s2[1]);
+                            for (int e = 0; e < 4; ++e) {
+                                bz = fma2(d[e], z[e], bz);
                                 q[e] = tg;
                             }
                         }
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) d[e] *= q[e];
-                    }
-                    if (drop) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            d[e] = philox_keep(bitsw, e, a.threshold) ? d[e] * a.inv_keep : 0.0f;
+                        for (int e = 0; e < 4; ++e) d[e] = mul2(d[e], q[e]);
                     }
                     if (post) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            gp[i][e] = fmaf(d[e], y[e] * u, gp[i][e]);
-                            c[i][e] = d[e] * w[e];
-                            s2[0] = fmaf(c[i][e], y[e], s2[0]);
+                        for (int e = 0; e < 4; ++e) {
+                            gp[i][e] = fma2(d[e], yu[e], gp[i][e]);
+                            c[i][e] = mul2(d[e], w[e]);
+                            cy = fma2(c[i][e], yu[e], cy);
                         }
                     } else {
-                        o.set(d);
+                        set2(o, d);
                         o.store(a.dy, row + v);
                     }
                 }
             }
         }
-        if (post || a.gate_mode == MOE_GATE_TOKEN) row_sum<2, ONEWARP>(s2, red, half);
-        if (a.gate_mode == MOE_GATE_TOKEN && tid == 0) static_cast<float*>(a.dgate)[t] = s2[1];
+        float s2[2] = {sum2(cy), sum2(bz)};
+        if (post || gate_mode == MOE_GATE_TOKEN) row_sum<2, ONEWARP>(s2, red, half);
+        if (gate_mode == MOE_GATE_TOKEN && tid == 0) static_cast<float*>(a.dgate)[t] = s2[1];
         if (post) {
-            const float mean_p = u * u * (s2[0] * a.inv_h);
+            // dy = u c - y u^2 mean(c y u): the sum above already holds one factor u
+            const F2 mean_p = f2(-u * u * (s2[0] * a.inv_h));
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int v = tid + i * step;
-                if (v < a.nvec) {
-                    float y[8];
-                    get(g.i_y, a.y, row, i, y);
+                if (v < nvec) {
+                    F2 y[4];
+                    get(at_y, a.y, row, i, y);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = u * (c[i][e] - y[e] * mean_p);
+                    for (int e = 0; e < 4; ++e) y[e] = fma2(y[e], mean_p, mul2(c[i][e], u2x));
                     Vec8<DT> o;
-                    o.set(y);
+                    set2(o, y);
                     o.store(a.dy, row + v);
                 }
             }
         }
-        if (g.stages > 0) {
-            fetch(stage, t + g.stages * rows);
-            if (++stage == g.stages) stage = 0;
+        if (has_ring) {
+            fetch(at, t + g.stages * rows);
+            at += stage_bytes;
+            if (at == ring0 + (uint32_t)g.stages * stage_bytes) at = ring0;
         }
     }
 
     // this row group's partial sums
     float* part = a.part + first * a.slots * (int64_t)a.H;
-    auto put = [&](int where, const float (&f)[V][8]) {
+    auto put = [&](int where, const F2 (&p)[V][4]) {
         if (where < 0) return;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int v = tid + i * step;
             if (v < a.nvec) {
                 float4* d = reinterpret_cast<float4*>(part + (int64_t)where * a.H) + 2 * v;
-                d[0] = make_float4(f[i][0], f[i][1], f[i][2], f[i][3]);
-                d[1] = make_float4(f[i][4], f[i][5], f[i][6], f[i][7]);
+                Vec8<MOE_F32> f;
+                set2(f, p[i]);
+                d[0] = f.a;
+                d[1] = f.b;
             }
         }
     };
@@ -544,20 +567,12 @@ RowShape row_shape(int nvec)
 
 constexpr int kWarpRows = 4;  // rows of a block in the one-warp form
 
-// the backward keeps 24 sums per vector in registers: one vector a thread up to H = 4096
-RowShape bwd_shape(int nvec)
-{
-    if (nvec <= 32) return {true, 1, 32};
-    if (nvec <= 512) return {false, 1, (nvec + 31) / 32 * 32};
-    return {false, 2, ((nvec + 1) / 2 + 31) / 32 * 32};
-}
-
 // row groups of the backward: a function of (T, H) alone, so that the order of the parameter
 // sums does not depend on the device (about 512 threads for each of a B200's 148 SMs, at least
 // two rows a group)
 int64_t bwd_groups(int64_t T, int32_t H)
 {
-    const RowShape s = bwd_shape(H / 8);
+    const RowShape s = row_shape(H / 8);
     int64_t per_sm = 512 / s.threads;
     if (per_sm < 1) per_sm = 1;
     int64_t g = 148 * per_sm;
@@ -599,16 +614,11 @@ cudaError_t norm_fwd(const NormArgs& a, cudaStream_t st)
     return launch_pdl(kernel, dim3((unsigned)a.T), dim3(s.threads), 0, st, a);
 }
 
-template <int DT, int V, int MAXT>
-cudaError_t norm_bwd_variant(const NormArgs& a, BwdRing g, dim3 grid, dim3 block, cudaStream_t st)
+template <int DT, int V, int MAXT, int MODE>
+cudaError_t norm_bwd_launch(const NormArgs& a, const BwdRing& g, dim3 grid, dim3 block, size_t smem,
+                            cudaStream_t st)
 {
-    auto kernel = residual_norm_bwd_kernel<DT, V, MAXT>;
-    const int threads = (int)(block.x * block.y);
-    const int per_sm = threads <= 512 ? 512 / threads : 1;
-    const size_t stage = (size_t)g.arrays * V * (DT == MOE_F32 ? 32 : 16) * threads;
-    g.stages = (int32_t)(225000 / per_sm / (stage > 0 ? stage : 1));
-    if (g.stages > 4) g.stages = 4;
-    const size_t smem = g.stages * stage;
+    auto kernel = residual_norm_bwd_kernel<DT, V, MAXT, MODE>;
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
@@ -622,6 +632,23 @@ cudaError_t norm_bwd_variant(const NormArgs& a, BwdRing g, dim3 grid, dim3 block
     return launch_pdl(kernel, grid, block, smem, st, a, g);
 }
 
+template <int DT, int V, int MAXT>
+cudaError_t norm_bwd_variant(const NormArgs& a, BwdRing g, dim3 grid, dim3 block, cudaStream_t st)
+{
+    const int threads = (int)(block.x * block.y);
+    const int per_sm = threads <= 512 ? 512 / threads : 1;
+    const size_t stage = (size_t)g.arrays * V * (DT == MOE_F32 ? 32 : 16) * threads;
+    g.stages = (int32_t)(225000 / per_sm / (stage > 0 ? stage : 1));
+    if (g.stages > 4) g.stages = 4;
+    const size_t smem = g.stages * stage;
+    if (a.w_post == nullptr || a.w_next == nullptr || a.dr == nullptr || !a.param_f32 ||
+        g.stages == 0)
+        return norm_bwd_launch<DT, V, MAXT, kBwdAny>(a, g, grid, block, smem, st);
+    return a.threshold != 0
+               ? norm_bwd_launch<DT, V, MAXT, kBwdAllDrop>(a, g, grid, block, smem, st)
+               : norm_bwd_launch<DT, V, MAXT, kBwdAll>(a, g, grid, block, smem, st);
+}
+
 template <int DT>
 cudaError_t norm_bwd(const NormArgs& a, int64_t groups, cudaStream_t st)
 {
@@ -632,16 +659,12 @@ cudaError_t norm_bwd(const NormArgs& a, int64_t groups, cudaStream_t st)
     g.i_dr = take(a.dr != nullptr);
     g.i_y = take(a.y != nullptr);
     g.i_gate = take(a.gate_mode == MOE_GATE_FULL);
-    const RowShape s = bwd_shape(a.nvec);
+    const RowShape s = row_shape(a.nvec);
     if (s.one_warp)
-        return norm_bwd_variant<DT, 1, 32>(a, g, dim3((unsigned)(groups / kWarpRows)),
+        return norm_bwd_variant<DT, 2, 32>(a, g, dim3((unsigned)(groups / kWarpRows)),
                                            dim3(32, kWarpRows), st);
     const dim3 grid((unsigned)groups), block(s.threads);
-    if (s.V == 1) {
-        if (s.threads <= 128) return norm_bwd_variant<DT, 1, 128>(a, g, grid, block, st);
-        if (s.threads <= 256) return norm_bwd_variant<DT, 1, 256>(a, g, grid, block, st);
-        return norm_bwd_variant<DT, 1, 512>(a, g, grid, block, st);
-    }
+    if (s.threads <= 256) return norm_bwd_variant<DT, 2, 256>(a, g, grid, block, st);
     if (s.threads <= 512) return norm_bwd_variant<DT, 2, 512>(a, g, grid, block, st);
     return norm_bwd_variant<DT, 2, 1024>(a, g, grid, block, st);
 }

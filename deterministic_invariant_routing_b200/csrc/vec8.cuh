@@ -10,6 +10,43 @@
 namespace moe {
 namespace {
 
+// Two fp32 values in one 64-bit register pair: the packed add, multiply and fma of sm_100
+// (each half rounded to nearest as its scalar form) halve the instructions of row kernels whose
+// arithmetic would otherwise take longer than their memory traffic.
+struct F2 {
+    uint64_t v;
+};
+
+__device__ __forceinline__ F2 f2(float lo, float hi)
+{
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
+__device__ __forceinline__ void unpack(F2 a, float& lo, float& hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b)
+{
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ float sum2(F2 a)
+{
+    float lo, hi;
+    unpack(a, lo, hi);
+    return lo + hi;
+}
+
 template <int DT>
 struct Vec8;
 
@@ -103,6 +140,24 @@ struct Vec8<MOE_F32> {
     }
 };
 
+// the 8 elements as four pairs
+template <int DT>
+__device__ __forceinline__ void get2(const Vec8<DT>& q, F2 (&f)[4])
+{
+    float s[8];
+    q.get(s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f2(s[2 * i], s[2 * i + 1]);
+}
+template <int DT>
+__device__ __forceinline__ void set2(Vec8<DT>& q, const F2 (&f)[4])
+{
+    float s[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpack(f[i], s[2 * i], s[2 * i + 1]);
+    q.set(s);
+}
+
 // 8 parameters starting at 8 * vec: fp32, or the activations' type
 template <int DT>
 __device__ __forceinline__ void load_param8(const void* p, bool f32, int64_t vec, float (&f)[8])
@@ -116,6 +171,15 @@ __device__ __forceinline__ void load_param8(const void* p, bool f32, int64_t vec
         v.load(p, vec);
         v.get(f);
     }
+}
+
+template <int DT>
+__device__ __forceinline__ void load_param2(const void* p, bool f32, int64_t vec, F2 (&f)[4])
+{
+    float s[8];
+    load_param8<DT>(p, f32, vec, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f2(s[2 * i], s[2 * i + 1]);
 }
 
 template <int DT>
