@@ -6,7 +6,7 @@
 //
 // n is taken from the rounded r, so the fused call gives the bits of the two calls it replaces.
 // Every sum is fp32 in an order that depends on H alone (a thread's own vectors, a shuffle
-// tree in each warp, the same tree over the warps): a token's row never depends on T or on its neighbours.
+// tree in each warp, the warps in order): a token's row never depends on T or on its neighbours.
 //
 // All of it is bound by memory: 4 row passes forward (x, y in; r, n out), 6 backward (y, r, dr,
 // dn in; dx, dy out). A row stays in the registers of one block (one warp up to H = 512), so
@@ -37,34 +37,78 @@ struct NormArgs {
     float eps, inv_h, residual_scale, branch_scale, inv_keep;  // inv_h: 1 / H
 };
 
-// Sums K values over a row's threads: a shuffle tree within each warp, then the same tree over
-// the warps' sums, read from shared memory by every warp. `red` alternates between two halves,
-// so one barrier a call is enough (a warp that writes a half again has passed the barrier of
-// the call in between, which every reader of that half had reached).
+// Sums K <= 4 values over a warp, the totals in every lane: each of the first shuffles adds two
+// values at once (a lane keeps one of them and gives the other away), so four values take 6
+// shuffles and 3 more to hand the totals out, not 20. The order of a value's sum is fixed.
 template <int K>
 __device__ __forceinline__ void warp_sum(float (&v)[K])
 {
+    constexpr uint32_t all = 0xffffffffu;
+    if (K == 1) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
+        for (int off = 16; off > 0; off >>= 1) v[0] += __shfl_xor_sync(all, v[0], off);
+        return;
+    }
+    const int lane = threadIdx.x & 31;
+    const bool hi = lane & 16;
+    float a = v[0], b = v[K > 1 ? 1 : 0];
+    float p = (hi ? b : a) + __shfl_xor_sync(all, hi ? a : b, 16);  // sums of v0 | v1
+    if (K > 2) {
+        const float c = v[K > 2 ? 2 : 0], d = K > 3 ? v[K > 3 ? 3 : 0] : 0.0f;
+        const float q = (hi ? d : c) + __shfl_xor_sync(all, hi ? c : d, 16);  // v2 | v3
+        const bool odd = lane & 8;
+        p = (odd ? q : p) + __shfl_xor_sync(all, odd ? p : q, 8);
+    } else {
+        p += __shfl_xor_sync(all, p, 8);
+    }
 #pragma unroll
-        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
+    for (int off = 4; off > 0; off >>= 1) p += __shfl_xor_sync(all, p, off);
+    v[0] = __shfl_sync(all, p, 0);
+    v[K > 1 ? 1 : 0] = __shfl_sync(all, p, 16);
+    if (K > 2) v[K > 2 ? 2 : 0] = __shfl_sync(all, p, 8);
+    if (K > 3) v[K > 3 ? 3 : 0] = __shfl_sync(all, p, 24);
 }
 
-template <int K, bool ONEWARP>
+// Sums K values over a row's threads: within each warp, then over the warps' sums in shared
+// memory -- up to 8 of them (MAXT <= 256) added by every thread from two 16-byte reads a value,
+// which the whole warp makes at one address; more by the shuffles again. `red` (cleared by
+// red_init()) alternates between two halves, so one barrier a call is enough (a
+// warp that writes a half again has passed the barrier of the call in between, which every
+// reader of that half had reached).
+constexpr int kRed = 32;  // floats per value and half
+
+template <int K, int MAXT>
 __device__ __forceinline__ void row_sum(float (&v)[K], float* red, int& half)
 {
     warp_sum<K>(v);
-    if (ONEWARP) return;
-    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float* b = red + half * 32 * K;
+    if (MAXT == 32) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float* b = red + half * kRed * K;
     half ^= 1;
     if (lane == 0)
 #pragma unroll
-        for (int k = 0; k < K; ++k) b[k * 32 + warp] = v[k];
+        for (int k = 0; k < K; ++k) b[k * kRed + warp] = v[k];
     __syncthreads();
+    if (MAXT <= 256) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = lane < warps ? b[k * 32 + lane] : 0.0f;
-    warp_sum<K>(v);
+        for (int k = 0; k < K; ++k) {
+            const float4 p = *reinterpret_cast<const float4*>(b + k * kRed);
+            const float4 q = *reinterpret_cast<const float4*>(b + k * kRed + 4);
+            v[k] = ((p.x + p.y) + (p.z + p.w)) + ((q.x + q.y) + (q.z + q.w));
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] = b[k * kRed + lane];
+        warp_sum<K>(v);
+    }
+}
+
+// zeros for the warps that a block does not have (visible after row_sum's first barrier)
+__device__ __forceinline__ void red_init(float* red, int floats)
+{
+    const int warps = blockDim.x >> 5;
+    for (int i = threadIdx.x; i < floats; i += blockDim.x)
+        if ((i & (kRed - 1)) >= warps) red[i] = 0.0f;
 }
 
 __device__ __forceinline__ float inv_rms(float ss, const NormArgs& a)
@@ -94,8 +138,9 @@ template <int DT, int V, int MAXT>
 __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT) residual_norm_kernel(NormArgs a)
 {
     constexpr bool ONEWARP = MAXT == 32;
-    __shared__ float red[2 * 32];
+    __shared__ __align__(16) float red[2 * kRed];
     int half = 0;
+    red_init(red, 2 * kRed);
     pdl_wait();
     const int64_t t = ONEWARP ? (int64_t)blockIdx.x * blockDim.y + threadIdx.y : blockIdx.x;
     if (t >= a.T) return;  // whole warps (ONEWARP); never otherwise
@@ -124,7 +169,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT) residual_norm_kernel(
                 }
             }
             float ss[1] = {sum2(acc)};
-            row_sum<1, ONEWARP>(ss, red, half);
+            row_sum<1, MAXT>(ss, red, half);
             scale *= inv_rms(ss[0], a);
         }
         if (a.gate_mode == MOE_GATE_TOKEN) scale *= load_param<DT>(a.gate, a.param_f32, t);
@@ -181,7 +226,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT) residual_norm_kernel(
         }
     }
     float ss[1] = {sum2(acc)};
-    row_sum<1, ONEWARP>(ss, red, half);
+    row_sum<1, MAXT>(ss, red, half);
     const F2 inv = f2(inv_rms(ss[0], a));
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -229,8 +274,9 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
     constexpr bool ONEWARP = MAXT == 32, ALL = MODE != kBwdAny;
     constexpr int W16 = DT == MOE_F32 ? 2 : 1;  // 16-byte words of a vector
     extern __shared__ uint4 ring[];
-    __shared__ float red[2 * 32 * 3];
+    __shared__ __align__(16) float red[2 * kRed * 3];
     int half = 0;
+    red_init(red, 2 * kRed * 3);
     pdl_wait();
     const int tid = threadIdx.x, step = blockDim.x;
     const int lin = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
@@ -250,6 +296,22 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
     for (int i = 0; i < V; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) gn[i][e] = gp[i][e] = gg[i][e] = f2(0.0f);
+    // with one vector a thread its weights and channel gate stay in registers
+    constexpr bool KEEP = ALL && V == 1;
+    F2 kn[4], kp[4], kg[4];
+    if (KEEP && tid < nvec) {
+        load_param2<DT>(a.w_next, true, tid, kn);
+        load_param2<DT>(a.w_post, true, tid, kp);
+        if (gate_mode == MOE_GATE_CHANNEL) load_param2<DT>(a.gate, true, tid, kg);
+    }
+    auto param = [&](const void* p, const F2 (&kept)[4], int v, F2 (&w)[4]) {
+        if (KEEP) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = kept[e];
+        } else {
+            load_param2<DT>(p, param_f32, v, w);
+        }
+    };
     Philox ph;
     if (drop) ph = philox_load(a.rng);
 
@@ -316,6 +378,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
         const int64_t row = t * nvec;
         if (has_ring) row_ready();
         F2 rr = f2(0.0f), wr = f2(0.0f), yy = f2(0.0f);  // r^2, w_next dn r, y^2
+        F2 kr[4], kd[4];  // KEEP: r and dn between the passes
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int v = tid + i * step;
@@ -324,11 +387,15 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
                 if (next) {
                     get(at_r, a.r, row, i, p);
                     get(at_dn, a.dn, row, i, q);
-                    load_param2<DT>(a.w_next, param_f32, v, w);
+                    param(a.w_next, kn, v, w);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         rr = fma2(p[e], p[e], rr);
                         wr = fma2(mul2(q[e], w[e]), p[e], wr);
+                        if (KEEP) {
+                            kr[e] = p[e];
+                            kd[e] = q[e];
+                        }
                     }
                 }
                 if (post) {
@@ -339,7 +406,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
             }
         }
         float s3[3] = {sum2(rr), sum2(wr), sum2(yy)};
-        if (next || post) row_sum<3, ONEWARP>(s3, red, half);
+        if (next || post) row_sum<3, MAXT>(s3, red, half);
         const float s = next ? inv_rms(s3[0], a) : 0.0f;
         const F2 s2x = f2(s), mean_n = f2(next ? -s * s * s * (s3[1] * a.inv_h) : 0.0f);
         const float u = post ? inv_rms(s3[2], a) : 1.0f;
@@ -362,9 +429,17 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
                 }
                 if (next) {
                     F2 p[4], w[4];
-                    get(at_r, a.r, row, i, p);
-                    get(at_dn, a.dn, row, i, q);
-                    load_param2<DT>(a.w_next, param_f32, v, w);
+                    if (KEEP) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            p[e] = kr[e];
+                            q[e] = kd[e];
+                        }
+                    } else {
+                        get(at_r, a.r, row, i, p);
+                        get(at_dn, a.dn, row, i, q);
+                    }
+                    param(a.w_next, kn, v, w);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const F2 k = mul2(q[e], s2x);
@@ -388,7 +463,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
                         d[e] = mul2(d[e], bscale);
                         yu[e] = mul2(yu[e], u2x);
                     }
-                    if (post) load_param2<DT>(a.w_post, param_f32, v, w);
+                    if (post) param(a.w_post, kp, v, w);
                     if (drop) drop2(bitsw, threshold, d);
                     if (gate_mode != MOE_GATE_NONE) {
                         // b z: the factor 1 / P(keep) of z is already in d, dropped ones are 0
@@ -403,7 +478,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
                             set2(o, z);
                             o.store(a.dgate, row + v);
                         } else if (gate_mode == MOE_GATE_CHANNEL) {
-                            load_param2<DT>(a.gate, param_f32, v, q);
+                            param(a.gate, kg, v, q);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) gg[i][e] = fma2(d[e], z[e], gg[i][e]);
                         } else {
@@ -431,7 +506,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
             }
         }
         float s2[2] = {sum2(cy), sum2(bz)};
-        if (post || gate_mode == MOE_GATE_TOKEN) row_sum<2, ONEWARP>(s2, red, half);
+        if (post || gate_mode == MOE_GATE_TOKEN) row_sum<2, MAXT>(s2, red, half);
         if (gate_mode == MOE_GATE_TOKEN && tid == 0) static_cast<float*>(a.dgate)[t] = s2[1];
         if (post) {
             // dy = u c - y u^2 mean(c y u): the sum above already holds one factor u
@@ -567,12 +642,20 @@ RowShape row_shape(int nvec)
 
 constexpr int kWarpRows = 4;  // rows of a block in the one-warp form
 
+// the backward: one vector a thread (24 sums and 24 weights in registers) up to H = 4096
+RowShape bwd_shape(int nvec)
+{
+    if (nvec <= 32) return {true, 1, 32};
+    if (nvec <= 512) return {false, 1, (nvec + 31) / 32 * 32};
+    return {false, 2, ((nvec + 1) / 2 + 31) / 32 * 32};
+}
+
 // row groups of the backward: a function of (T, H) alone, so that the order of the parameter
 // sums does not depend on the device (about 512 threads for each of a B200's 148 SMs, at least
 // two rows a group)
 int64_t bwd_groups(int64_t T, int32_t H)
 {
-    const RowShape s = row_shape(H / 8);
+    const RowShape s = bwd_shape(H / 8);
     int64_t per_sm = 512 / s.threads;
     if (per_sm < 1) per_sm = 1;
     int64_t g = 148 * per_sm;
@@ -659,12 +742,14 @@ cudaError_t norm_bwd(const NormArgs& a, int64_t groups, cudaStream_t st)
     g.i_dr = take(a.dr != nullptr);
     g.i_y = take(a.y != nullptr);
     g.i_gate = take(a.gate_mode == MOE_GATE_FULL);
-    const RowShape s = row_shape(a.nvec);
+    const RowShape s = bwd_shape(a.nvec);
     if (s.one_warp)
-        return norm_bwd_variant<DT, 2, 32>(a, g, dim3((unsigned)(groups / kWarpRows)),
+        return norm_bwd_variant<DT, 1, 32>(a, g, dim3((unsigned)(groups / kWarpRows)),
                                            dim3(32, kWarpRows), st);
     const dim3 grid((unsigned)groups), block(s.threads);
-    if (s.threads <= 256) return norm_bwd_variant<DT, 2, 256>(a, g, grid, block, st);
+    if (s.V == 1)
+        return s.threads <= 256 ? norm_bwd_variant<DT, 1, 256>(a, g, grid, block, st)
+                                : norm_bwd_variant<DT, 1, 512>(a, g, grid, block, st);
     if (s.threads <= 512) return norm_bwd_variant<DT, 2, 512>(a, g, grid, block, st);
     return norm_bwd_variant<DT, 2, 1024>(a, g, grid, block, st);
 }

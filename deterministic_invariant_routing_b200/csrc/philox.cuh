@@ -25,7 +25,9 @@ struct Philox {
 // rng: device int64[2], (seed, offset)
 __device__ __forceinline__ Philox philox_load(const int64_t* rng)
 {
-    const uint64_t seed = (uint64_t)rng[0], off = (uint64_t)rng[1];
+    // one lane's copy for all: the key schedule then stays in uniform registers
+    const uint64_t seed = __shfl_sync(0xffffffffu, (unsigned long long)rng[0], 0);
+    const uint64_t off = __shfl_sync(0xffffffffu, (unsigned long long)rng[1], 0);
     return Philox{(uint32_t)seed, (uint32_t)(seed >> 32), (uint32_t)off, (uint32_t)(off >> 32)};
 }
 
