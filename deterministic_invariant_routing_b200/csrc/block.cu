@@ -16,6 +16,7 @@
 // Parameter gradients are column sums over tokens: block b of a grid whose size is a function
 // of (T, H) adds rows b, b + blocks, ... into its registers and writes one partial row; a second
 // kernel sums the partials in order. No atomics: the bits repeat, on any device.
+#include "fast_div.cuh"
 #include "philox.cuh"
 #include "vec8.cuh"
 
@@ -133,11 +134,20 @@ __device__ __forceinline__ void drop2(const uint32_t (&w)[4], uint32_t threshold
     }
 }
 
+// What a call has: kAny looks as it goes; kAll and kAllDrop are the usual call, with both norms
+// (backward: dr and room for the ring too) and fp32 parameters, without and with dropout. Bound
+// by instructions, the looking costs: a fifth of the backward's were branches and their constants.
+enum { kAny = 0, kAll = 1, kAllDrop = 2 };
+
 // one row per block of blockDim.x <= MAXT threads, or (MAXT = 32) one per warp, threadIdx.y the row
-template <int DT, int V, int MAXT>
-__global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT) residual_norm_kernel(NormArgs a)
+template <int DT, int V, int MAXT, int MODE>
+__global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT)
+    residual_norm_kernel(const __grid_constant__ NormArgs a)
 {
-    constexpr bool ONEWARP = MAXT == 32;
+    constexpr bool ONEWARP = MAXT == 32, ALL = MODE != kAny;
+    const bool post = ALL || a.w_post != nullptr, next = ALL || a.w_next != nullptr;
+    const bool branch = ALL || a.y != nullptr, param_f32 = ALL || a.param_f32;
+    const bool drop = MODE == kAllDrop || (MODE == kAny && a.threshold != 0);
     __shared__ __align__(16) float red[2 * kRed];
     int half = 0;
     red_init(red, 2 * kRed);
@@ -152,12 +162,12 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT) residual_norm_kernel(
         const int v = tid + i * step;
         if (v < a.nvec) {
             x[i].load(a.x, row + v);
-            if (a.y != nullptr) y[i].load(a.y, row + v);
+            if (branch) y[i].load(a.y, row + v);
         }
     }
-    if (a.y != nullptr) {
-        float scale = a.branch_scale * (a.threshold ? a.inv_keep : 1.0f);
-        if (a.w_post != nullptr) {
+    if (branch) {
+        float scale = a.branch_scale * (drop ? a.inv_keep : 1.0f);
+        if (post) {
             F2 acc = f2(0.0f);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
@@ -172,10 +182,18 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT) residual_norm_kernel(
             row_sum<1, MAXT>(ss, red, half);
             scale *= inv_rms(ss[0], a);
         }
-        if (a.gate_mode == MOE_GATE_TOKEN) scale *= load_param<DT>(a.gate, a.param_f32, t);
-        Philox ph;
-        if (a.threshold) ph = philox_load(a.rng);
-        const uint32_t rid = a.threshold ? row_id(a, t) : 0u;
+        if (a.gate_mode == MOE_GATE_TOKEN) scale *= load_param<DT>(a.gate, param_f32, t);
+        uint32_t mask[V][4];
+        if (drop) {
+            const uint32_t rid = row_id(a, t);
+            uint32_t col[V], rows[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                col[i] = (uint32_t)(tid + i * step);
+                rows[i] = rid;
+            }
+            philox8n<V>(philox_load(a.rng), col, rows, mask);
+        }
         const F2 sc = f2(scale), rs = f2(a.residual_scale);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -185,19 +203,15 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT) residual_norm_kernel(
                 get2(y[i], z);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) z[e] = mul2(z[e], sc);
-                if (a.w_post != nullptr) {
-                    load_param2<DT>(a.w_post, a.param_f32, v, q);
+                if (post) {
+                    load_param2<DT>(a.w_post, param_f32, v, q);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) z[e] = mul2(z[e], q[e]);
                 }
-                if (a.threshold) {
-                    uint32_t w[4];
-                    philox8(ph, (uint32_t)v, rid, w);
-                    drop2(w, a.threshold, z);
-                }
+                if (drop) drop2(mask[i], a.threshold, z);
                 if (a.gate_mode >= MOE_GATE_CHANNEL && a.gate_mode != MOE_GATE_TOKEN) {
                     if (a.gate_mode == MOE_GATE_CHANNEL) {
-                        load_param2<DT>(a.gate, a.param_f32, v, q);
+                        load_param2<DT>(a.gate, param_f32, v, q);
                     } else {
                         Vec8<DT> g;
                         g.load(a.gate, row + v);
@@ -214,7 +228,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT) residual_norm_kernel(
             }
         }
     }
-    if (a.w_next == nullptr) return;
+    if (!next) return;
     F2 acc = f2(0.0f);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -234,7 +248,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT) residual_norm_kernel(
         if (v < a.nvec) {
             F2 q[4], w[4];
             get2(x[i], q);
-            load_param2<DT>(a.w_next, a.param_f32, v, w);
+            load_param2<DT>(a.w_next, param_f32, v, w);
 #pragma unroll
             for (int e = 0; e < 4; ++e) q[e] = mul2(mul2(q[e], inv), w[e]);
             set2(x[i], q);
@@ -260,18 +274,13 @@ struct BwdRing {
     int32_t i_r, i_dn, i_dr, i_y, i_gate; // place of each array in a stage, -1: absent
 };
 
-// MODE: kBwdAny looks at what is present as it goes; kBwdAll and kBwdAllDrop are the usual call,
-// with both norms, dr, fp32 parameters and room for the ring, without and with dropout. Bound by
-// instructions, the looking costs: of 100 per element a fifth were branches and their constants.
-enum { kBwdAny = 0, kBwdAll = 1, kBwdAllDrop = 2 };
-
 template <int DT, int V, int MAXT, int MODE>
 __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
                                                            : MAXT == 256 ? 2
                                                                          : 1)
     residual_norm_bwd_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ BwdRing g)
 {
-    constexpr bool ONEWARP = MAXT == 32, ALL = MODE != kBwdAny;
+    constexpr bool ONEWARP = MAXT == 32, ALL = MODE != kAny;
     constexpr int W16 = DT == MOE_F32 ? 2 : 1;  // 16-byte words of a vector
     extern __shared__ uint4 ring[];
     __shared__ __align__(16) float red[2 * kRed * 3];
@@ -284,7 +293,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
     const int64_t first = ONEWARP ? (int64_t)blockIdx.x * blockDim.y + threadIdx.y : blockIdx.x;
     const bool post = ALL || a.w_post != nullptr, next = ALL || a.w_next != nullptr;
     const bool branch = ALL || a.y != nullptr, has_dr = ALL || a.dr != nullptr;
-    const bool drop = MODE == kBwdAllDrop || (MODE == kBwdAny && a.threshold != 0);
+    const bool drop = MODE == kAllDrop || (MODE == kAny && a.threshold != 0);
     const bool has_ring = ALL || g.stages > 0, param_f32 = ALL || a.param_f32;
     const int nvec = a.nvec, gate_mode = a.gate_mode;
     const uint32_t threshold = a.threshold;
@@ -589,39 +598,44 @@ __global__ void __launch_bounds__(32 * kSlices) param_grad_kernel(ReduceArgs a)
     }
 }
 
-// out = keep ? x / probability : 0, each thread kVec vectors of 8, a block's width apart
+// out = keep ? x / probability : 0, each thread kVec vectors of 8, a block's width apart. A bf16
+// tensor moves 4 bytes an element and takes about 20 integer instructions for it (half of
+// Philox's are 32 x 32 -> 64 bit products): the arithmetic pipes bound it, at 30 % of the
+// memory rate short of them.
 constexpr int kVec = 4;
 
 template <int DT>
-__global__ void __launch_bounds__(256) dropout_kernel(const void* x, void* out, int64_t T,
-                                                      int32_t nvec, uint32_t threshold,
+__global__ void __launch_bounds__(256) dropout_kernel(const void* x, void* out, int64_t total,
+                                                      FastDiv nvec, uint32_t threshold,
                                                       float inv_keep, const int64_t* rng,
                                                       uint32_t first_row, const int32_t* row_ids)
 {
     pdl_wait();
     const Philox ph = philox_load(rng);
-    const int64_t total = T * nvec;
     const int64_t base = (int64_t)blockIdx.x * (256 * kVec) + threadIdx.x;
     Vec8<DT> q[kVec];
 #pragma unroll
     for (int i = 0; i < kVec; ++i)
         if (base + 256 * i < total) q[i].load(x, base + 256 * i);
+    uint32_t col[kVec], row[kVec], w[kVec][4];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-        const int64_t g = base + 256 * i;
-        if (g < total) {
-            const int64_t t = total <= 0xffffffffll ? (int64_t)((uint32_t)g / (uint32_t)nvec)
-                                                    : g / nvec;
-            const uint32_t v = (uint32_t)(g - t * nvec);
-            uint32_t w[4];
-            philox8(ph, v, row_ids != nullptr ? (uint32_t)row_ids[t] : first_row + (uint32_t)t, w);
+        const int64_t g = base + 256 * i < total ? base + 256 * i : 0;
+        const int64_t t = quotient(g, nvec, total <= 0x7fffffffll);
+        col[i] = (uint32_t)(g - t * nvec.d);
+        row[i] = row_ids != nullptr ? (uint32_t)row_ids[t] : first_row + (uint32_t)t;
+    }
+    philox8n<kVec>(ph, col, row, w);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        if (base + 256 * i < total) {
             float f[8];
             q[i].get(f);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                f[e] = philox_keep(w, e, threshold) ? f[e] * inv_keep : 0.0f;
+                f[e] = philox_keep(w[i], e, threshold) ? f[e] * inv_keep : 0.0f;
             q[i].set(f);
-            q[i].store(out, g);
+            q[i].store(out, base + 256 * i);
         }
     }
 }
@@ -682,19 +696,29 @@ NormArgs base_args(const moe_norm_cfg& c)
     return a;
 }
 
+template <int DT, int V, int MAXT>
+cudaError_t norm_fwd_variant(const NormArgs& a, dim3 grid, dim3 block, cudaStream_t st)
+{
+    const bool all = a.w_post != nullptr && a.w_next != nullptr && a.param_f32;
+    auto kernel = !all               ? residual_norm_kernel<DT, V, MAXT, kAny>
+                  : a.threshold == 0 ? residual_norm_kernel<DT, V, MAXT, kAll>
+                                     : residual_norm_kernel<DT, V, MAXT, kAllDrop>;
+    return launch_pdl(kernel, grid, block, 0, st, a);
+}
+
 template <int DT>
 cudaError_t norm_fwd(const NormArgs& a, cudaStream_t st)
 {
     const RowShape s = row_shape(a.nvec);
     if (s.one_warp) {
         const dim3 grid((unsigned)((a.T + kWarpRows - 1) / kWarpRows)), block(32, kWarpRows);
-        return s.V == 1 ? launch_pdl(residual_norm_kernel<DT, 1, 32>, grid, block, 0, st, a)
-                        : launch_pdl(residual_norm_kernel<DT, 2, 32>, grid, block, 0, st, a);
+        return s.V == 1 ? norm_fwd_variant<DT, 1, 32>(a, grid, block, st)
+                        : norm_fwd_variant<DT, 2, 32>(a, grid, block, st);
     }
-    auto kernel = s.threads <= 256   ? residual_norm_kernel<DT, 2, 256>
-                  : s.threads <= 512 ? residual_norm_kernel<DT, 2, 512>
-                                     : residual_norm_kernel<DT, 2, 1024>;
-    return launch_pdl(kernel, dim3((unsigned)a.T), dim3(s.threads), 0, st, a);
+    const dim3 grid((unsigned)a.T), block(s.threads);
+    if (s.threads <= 256) return norm_fwd_variant<DT, 2, 256>(a, grid, block, st);
+    if (s.threads <= 512) return norm_fwd_variant<DT, 2, 512>(a, grid, block, st);
+    return norm_fwd_variant<DT, 2, 1024>(a, grid, block, st);
 }
 
 template <int DT, int V, int MAXT, int MODE>
@@ -726,10 +750,10 @@ cudaError_t norm_bwd_variant(const NormArgs& a, BwdRing g, dim3 grid, dim3 block
     const size_t smem = g.stages * stage;
     if (a.w_post == nullptr || a.w_next == nullptr || a.dr == nullptr || !a.param_f32 ||
         g.stages == 0)
-        return norm_bwd_launch<DT, V, MAXT, kBwdAny>(a, g, grid, block, smem, st);
+        return norm_bwd_launch<DT, V, MAXT, kAny>(a, g, grid, block, smem, st);
     return a.threshold != 0
-               ? norm_bwd_launch<DT, V, MAXT, kBwdAllDrop>(a, g, grid, block, smem, st)
-               : norm_bwd_launch<DT, V, MAXT, kBwdAll>(a, g, grid, block, smem, st);
+               ? norm_bwd_launch<DT, V, MAXT, kAllDrop>(a, g, grid, block, smem, st)
+               : norm_bwd_launch<DT, V, MAXT, kAll>(a, g, grid, block, smem, st);
 }
 
 template <int DT>
@@ -854,14 +878,14 @@ cudaError_t launch_dropout(int64_t T, int32_t H, int dtype, double p, const void
     const uint32_t fr = (uint32_t)first_row;
     switch (dtype) {
         case MOE_BF16:
-            return launch_pdl(dropout_kernel<MOE_BF16>, grid, dim3(256), 0, st, x, out, T, nvec,
-                              th, inv, rng, fr, row_ids);
+            return launch_pdl(dropout_kernel<MOE_BF16>, grid, dim3(256), 0, st, x, out, total,
+                              FastDiv((uint32_t)nvec), th, inv, rng, fr, row_ids);
         case MOE_F16:
-            return launch_pdl(dropout_kernel<MOE_F16>, grid, dim3(256), 0, st, x, out, T, nvec,
-                              th, inv, rng, fr, row_ids);
+            return launch_pdl(dropout_kernel<MOE_F16>, grid, dim3(256), 0, st, x, out, total,
+                              FastDiv((uint32_t)nvec), th, inv, rng, fr, row_ids);
         default:
-            return launch_pdl(dropout_kernel<MOE_F32>, grid, dim3(256), 0, st, x, out, T, nvec,
-                              th, inv, rng, fr, row_ids);
+            return launch_pdl(dropout_kernel<MOE_F32>, grid, dim3(256), 0, st, x, out, total,
+                              FastDiv((uint32_t)nvec), th, inv, rng, fr, row_ids);
     }
 }
 

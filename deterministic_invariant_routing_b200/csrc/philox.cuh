@@ -31,24 +31,49 @@ __device__ __forceinline__ Philox philox_load(const int64_t* rng)
     return Philox{(uint32_t)seed, (uint32_t)(seed >> 32), (uint32_t)off, (uint32_t)(off >> 32)};
 }
 
+__device__ __forceinline__ void philox_round(uint32_t& c0, uint32_t& c1, uint32_t& c2,
+                                             uint32_t& c3, uint32_t k0, uint32_t k1)
+{
+    const uint64_t p0 = (uint64_t)c0 * 0xD2511F53u, p1 = (uint64_t)c2 * 0xCD9E8D57u;
+    c0 = (uint32_t)(p1 >> 32) ^ c1 ^ k0;
+    c1 = (uint32_t)p1;
+    c2 = (uint32_t)(p0 >> 32) ^ c3 ^ k1;
+    c3 = (uint32_t)p0;
+}
+
 __device__ __forceinline__ void philox8(const Philox& g, uint32_t col8, uint32_t row,
                                         uint32_t (&w)[4])
 {
-    uint32_t c0 = col8, c1 = row, c2 = g.c2, c3 = g.c3, k0 = g.k0, k1 = g.k1;
+    w[0] = col8;
+    w[1] = row;
+    w[2] = g.c2;
+    w[3] = g.c3;
+#pragma unroll
+    for (uint32_t i = 0; i < 10; ++i)
+        philox_round(w[0], w[1], w[2], w[3], g.k0 + i * 0x9E3779B9u, g.k1 + i * 0xBB67AE85u);
+}
+
+// N vectors at once: a round's keys are formed once for all of them, and their rounds interleave
+template <int N>
+__device__ __forceinline__ void philox8n(const Philox& g, const uint32_t (&col8)[N],
+                                         const uint32_t (&row)[N], uint32_t (&w)[N][4])
+{
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        w[n][0] = col8[n];
+        w[n][1] = row[n];
+        w[n][2] = g.c2;
+        w[n][3] = g.c3;
+    }
+    uint32_t k0 = g.k0, k1 = g.k1;
 #pragma unroll
     for (int i = 0; i < 10; ++i) {
-        const uint64_t p0 = (uint64_t)c0 * 0xD2511F53u, p1 = (uint64_t)c2 * 0xCD9E8D57u;
-        c0 = (uint32_t)(p1 >> 32) ^ c1 ^ k0;
-        c1 = (uint32_t)p1;
-        c2 = (uint32_t)(p0 >> 32) ^ c3 ^ k1;
-        c3 = (uint32_t)p0;
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            philox_round(w[n][0], w[n][1], w[n][2], w[n][3], k0, k1);
         k0 += 0x9E3779B9u;
         k1 += 0xBB67AE85u;
     }
-    w[0] = c0;
-    w[1] = c1;
-    w[2] = c2;
-    w[3] = c3;
 }
 
 // whether element e (0..7) of the vector is kept
