@@ -113,6 +113,8 @@ _lib = None
 def load():
     """The loaded library (raises if it is not built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

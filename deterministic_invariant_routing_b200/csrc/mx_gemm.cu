@@ -135,6 +135,12 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
+// bring a tensor map (a kernel parameter) into the cache that TMA reads it through
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
 // a value that every lane of the warp holds, known to be the same in all of them
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
@@ -235,30 +241,36 @@ __global__ void __launch_bounds__(kXThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
+    if (warp == 0 && elect_one()) {
+        prefetch_map(&tmA);
+        prefetch_map(&tmA32);
+        prefetch_map(&tmB);
+        prefetch_map(&tmSA);
+        prefetch_map(&tmSB);
+        prefetch_map(&tmO);
+    }
     if (warp == 1) tmem_alloc_pair(smem_u32(misc), kXCols);
     pdl_wait();
+    // the groups' offsets, clamped, by all threads at once; then one warp counts row tiles
+    for (int g = threadIdx.x; g <= G; g += kXThreads) {
+        int o = args.offsets != nullptr ? args.offsets[g] : (g == 0 ? 0 : (int)args.rows);
+        if (o < 0 || o > args.rows) {
+            if (blockIdx.x == 0) status_add(args.status, MOE_ST_BAD_ROWS, 1);
+            o = o < 0 ? 0 : (int)args.rows;
+        }
+        offs[g] = o;
+    }
+    __syncthreads();
     if (warp == 2) {
         bool bad = false;
-        auto row_off = [&](int g) -> int {
-            if (args.offsets == nullptr) return g == 0 ? 0 : (int)args.rows;
-            const int o = args.offsets[g];
-            if (o < 0 || o > args.rows) bad = true;
-            return o < 0 ? 0 : (o > args.rows ? (int)args.rows : o);
-        };
-        auto tiles_of = [&](int beg, int end) -> int {
-            if (end < beg) bad = true;
-            return mx_row_tiles(beg, end);
-        };
         const int per = (G + 31) / 32;
         const int beg = lane * per < G ? lane * per : G;
         const int end = beg + per < G ? beg + per : G;
         int sum = 0;
         for (int g = beg; g < end; ++g) {
-            const int r0 = row_off(g);
-            offs[g] = r0;
-            sum += tiles_of(r0, row_off(g + 1));
+            if (offs[g + 1] < offs[g]) bad = true;
+            sum += mx_row_tiles(offs[g], offs[g + 1]);
         }
-        if (lane == 0) offs[G] = row_off(G);
         int incl = sum;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -268,7 +280,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         int run = incl - sum;
         for (int g = beg; g < end; ++g) {
             prefix[g] = run;
-            run += tiles_of(row_off(g), row_off(g + 1));
+            run += mx_row_tiles(offs[g], offs[g + 1]);
         }
         if (lane == 31) prefix[G] = incl;
         if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0)

@@ -70,7 +70,7 @@ class Config:
 
 
 def _p(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()  # an int, taken as a pointer by the signatures
 
 
 def _stream(dev: torch.device):
@@ -78,6 +78,9 @@ def _stream(dev: torch.device):
 
 
 def _need(t, name, dtype, shape, dev):
+    if t is not None and t.dtype is dtype and t.shape == shape and t.device == dev and \
+            t.is_contiguous():
+        return t
     if t is None:
         raise MoeError(f"{name} is required")
     if t.dtype != dtype:
@@ -259,24 +262,27 @@ _DTYPES = {torch.bfloat16: N.MOE_BF16, torch.float16: N.MOE_F16, torch.float32: 
 
 
 def _call(dev: torch.device, fn, *args):
-    """fn(*args, stream) on dev's current stream, with dev the current device."""
+    """fn(*args, stream) on dev's current stream, with dev the current device. (The raw calls:
+    torch.cuda's own wrappers cost as much as the launch of a small kernel.)"""
     if dev.type != "cuda":
         raise MoeError(f"tensors on {dev}, expected a CUDA device")
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        return fn(*args, _stream(dev))
+    i = dev.index
+    if i == torch._C._cuda_getDevice():
+        return fn(*args, torch._C._cuda_getCurrentRawStream(i))
     with torch.cuda.device(dev):
-        return fn(*args, _stream(dev))
+        return fn(*args, torch._C._cuda_getCurrentRawStream(i))
 
 
-def _act(t, name, shape=None, dtype=None, dev=None):
+def _act(t, name):
     """A contiguous 2-D activation of a supported type."""
     if t is None:
         raise MoeError(f"{name} is required")
     if t.dtype not in _DTYPES or t.dim() != 2:
         raise MoeError(f"{name}: a 2-D bf16, fp16 or fp32 tensor is expected, got {t.dtype} "
                        f"{tuple(t.shape)}")
-    return _need(t, name, t.dtype if dtype is None else dtype, t.shape if shape is None else shape,
-                 t.device if dev is None else dev)
+    if not t.is_contiguous():
+        raise MoeError(f"{name} must be contiguous")
+    return t
 
 
 def rng_state(seed: int, offset: int = 0, device="cuda") -> torch.Tensor:
@@ -288,37 +294,43 @@ def rng_state(seed: int, offset: int = 0, device="cuda") -> torch.Tensor:
 
 def _norm_setup(x, y, w_post, gate, w_next, eps, residual_scale, branch_scale, p, rng, first_row,
                 row_ids):
-    """Checks shared by residual_norm and its backward: (cfg, parameter and gate dtype checks)."""
-    T, H = x.shape
-    dev = x.device
-    params = [t for t in (w_post, w_next) if t is not None]
-    mode = N.MOE_GATE_NONE
-    if gate is not None:
-        shapes = {(H,): N.MOE_GATE_CHANNEL, (T, 1): N.MOE_GATE_TOKEN, (T, H): N.MOE_GATE_FULL}
-        mode = shapes.get(tuple(gate.shape))
-        if mode is None:
-            raise MoeError(f"gate: shape {tuple(gate.shape)}, expected ({H},), ({T}, 1) or "
-                           f"({T}, {H})")
-        if mode == N.MOE_GATE_FULL:
-            _need(gate, "gate", x.dtype, (T, H), dev)
-        else:
-            params.append(gate)
-    pd = params[0].dtype if params else torch.float32
-    if pd not in (torch.float32, x.dtype):
-        raise MoeError(f"parameters: dtype {pd}, expected torch.float32 or {x.dtype}")
-    _opt(w_post, "w_post", pd, (H,), dev)
-    _opt(w_next, "w_next", pd, (H,), dev)
-    if gate is not None and mode != N.MOE_GATE_FULL:
-        _need(gate, "gate", pd, gate.shape, dev)
-    if y is None and (w_post is not None or gate is not None or p or w_next is None or
-                      residual_scale != 1.0):
+    """The checks that residual_norm and its backward share; their configuration."""
+    shape, dt, dev = x.shape, x.dtype, x.device
+    T, H = shape
+    if y is not None:
+        _need(y, "y", dt, shape, dev)
+    elif w_post is not None or gate is not None or p or w_next is None or residual_scale != 1.0:
         raise MoeError("without y there is only the norm: w_next is required, and w_post, gate, "
                        "p and residual_scale do not apply")
+    mode, small_gate = N.MOE_GATE_NONE, None
+    if gate is not None:
+        g = tuple(gate.shape)
+        if g == (H,):
+            mode, small_gate = N.MOE_GATE_CHANNEL, gate
+        elif g == (T, 1):
+            mode, small_gate = N.MOE_GATE_TOKEN, gate
+        elif g == (T, H):
+            mode = N.MOE_GATE_FULL
+            _need(gate, "gate", dt, shape, dev)
+        else:
+            raise MoeError(f"gate: shape {g}, expected ({H},), ({T}, 1) or ({T}, {H})")
+    pd = None
+    for t, name, want in ((w_post, "w_post", (H,)), (w_next, "w_next", (H,)),
+                          (small_gate, "gate", None)):
+        if t is None:
+            continue
+        if pd is None:
+            pd = t.dtype
+            if pd is not torch.float32 and pd is not dt:
+                raise MoeError(f"{name}: dtype {pd}, expected torch.float32 or {dt}")
+        _need(t, name, pd, t.shape if want is None else want, dev)
     if p:
         _need(rng, "rng", torch.int64, (2,), dev)
-    _opt(row_ids, "row_ids", torch.int32, (T,), dev)
-    return N.MoeNormCfg(T, int(first_row), float(p), H, _DTYPES[x.dtype], _DTYPES[pd], mode,
-                        float(eps), float(residual_scale), float(branch_scale))
+    if row_ids is not None:
+        _need(row_ids, "row_ids", torch.int32, (T,), dev)
+    code = _DTYPES[dt]
+    return N.MoeNormCfg(T, first_row, p, H, code, code if pd is dt else N.MOE_F32, mode, eps,
+                        residual_scale, branch_scale)
 
 
 def residual_norm(x, y=None, w_post=None, gate=None, w_next=None, eps: float = 1e-6,
@@ -335,18 +347,22 @@ def residual_norm(x, y=None, w_post=None, gate=None, w_next=None, eps: float = 1
     (r may be x, n may be y). Returns (r, n), n None without w_next; r is x without y."""
     _act(x, "x")
     dev = x.device
-    if y is not None:
-        _need(y, "y", x.dtype, x.shape, dev)
     cfg = _norm_setup(x, y, w_post, gate, w_next, eps, residual_scale, branch_scale, p, rng,
                       first_row, row_ids)
-    if y is not None:
-        r = torch.empty_like(x) if r is None else _need(r, "r", x.dtype, x.shape, dev)
-    elif r is not None:
-        raise MoeError("without y, r is x: no output to write")
-    if w_next is not None:
-        n = torch.empty_like(x) if n is None else _need(n, "n", x.dtype, x.shape, dev)
-    elif n is not None:
-        raise MoeError("n needs w_next")
+    if y is None:
+        if r is not None:
+            raise MoeError("without y, r is x: no output to write")
+    elif r is None:
+        r = torch.empty_like(x)
+    else:
+        _need(r, "r", x.dtype, x.shape, dev)
+    if w_next is None:
+        if n is not None:
+            raise MoeError("n needs w_next")
+    elif n is None:
+        n = torch.empty_like(x)
+    else:
+        _need(n, "n", x.dtype, x.shape, dev)
     _rc(_call(dev, N.load().moe_residual_norm, ctypes.byref(cfg), _p(x), _p(y), _p(w_post),
               _p(gate), _p(w_next), _p(rng), _p(row_ids), _p(r), _p(n)), "moe_residual_norm")
     return (x if y is None else r), n
@@ -362,36 +378,30 @@ def residual_norm_backward(r, y=None, dr=None, dn=None, w_post=None, gate=None, 
     be None. dx, dy and a [T,H] gate's gradient have r's type, the others are fp32. The norm
     statistics and the dropout mask are recomputed; nothing else is kept from the forward."""
     _act(r, "r")
-    dev = r.device
-    T, H = r.shape
-    if y is not None:
-        _need(y, "y", r.dtype, r.shape, dev)
+    dev, dt, shape = r.device, r.dtype, r.shape
     cfg = _norm_setup(r, y, w_post, gate, w_next, eps, residual_scale, branch_scale, p, rng,
                       first_row, row_ids)
-    _opt(dr, "dr", r.dtype, r.shape, dev)
-    _opt(dn, "dn", r.dtype, r.shape, dev)
+    _opt(dr, "dr", dt, shape, dev)
+    _opt(dn, "dn", dt, shape, dev)
     if (dn is None) != (w_next is None):
         raise MoeError("dn is given exactly with w_next")
     if dr is None and dn is None:
         raise MoeError("dr or dn is required")
-    lib = N.load()
-    g = {"dx": torch.empty_like(r)}
-    if y is not None:
-        g["dy"] = torch.empty_like(r)
-    if w_post is not None:
-        g["dw_post"] = torch.empty(H, dtype=torch.float32, device=dev)
-    if gate is not None:
-        g["dgate"] = torch.empty(gate.shape, dtype=gate.dtype if cfg.gate == N.MOE_GATE_FULL
-                                 else torch.float32, device=dev)
-    if w_next is not None:
-        g["dw_next"] = torch.empty(H, dtype=torch.float32, device=dev)
-    nbytes = lib.moe_residual_norm_workspace_bytes(ctypes.byref(cfg))
+    lib, f32 = N.load(), torch.float32
+    dx = torch.empty_like(r)
+    dy = None if y is None else torch.empty_like(r)
+    dw_post = None if w_post is None else torch.empty_like(w_post, dtype=f32)
+    dgate = None if gate is None else torch.empty_like(
+        gate, dtype=dt if cfg.gate == N.MOE_GATE_FULL else f32)
+    dw_next = None if w_next is None else torch.empty_like(w_next, dtype=f32)
+    ref = ctypes.byref(cfg)
+    nbytes = lib.moe_residual_norm_workspace_bytes(ref)
     ws = _ws(nbytes, dev, None)
-    _rc(_call(dev, lib.moe_residual_norm_backward, ctypes.byref(cfg), _p(r), _p(y), _p(w_post),
-              _p(gate), _p(w_next), _p(rng), _p(row_ids), _p(dr), _p(dn), _p(g["dx"]),
-              _p(g.get("dy")), _p(g.get("dw_post")), _p(g.get("dgate")), _p(g.get("dw_next")),
-              _p(ws), nbytes), "moe_residual_norm_backward")
-    return g
+    _rc(_call(dev, lib.moe_residual_norm_backward, ref, _p(r), _p(y), _p(w_post), _p(gate),
+              _p(w_next), _p(rng), _p(row_ids), _p(dr), _p(dn), _p(dx), _p(dy), _p(dw_post),
+              _p(dgate), _p(dw_next), _p(ws), nbytes), "moe_residual_norm_backward")
+    g = {"dx": dx, "dy": dy, "dw_post": dw_post, "dgate": dgate, "dw_next": dw_next}
+    return {k: v for k, v in g.items() if v is not None}
 
 
 def dropout(x, p: float, rng, first_row: int = 0, row_ids=None, out=None):
@@ -400,12 +410,12 @@ def dropout(x, p: float, rng, first_row: int = 0, row_ids=None, out=None):
     row and the column alone; row t is first_row + t, or row_ids[t], so a token keeps its mask
     in any batch. The gradient is dropout(dout) with the same p, rng and rows. out may be x."""
     _act(x, "x")
-    dev = x.device
+    dev, (T, H) = x.device, x.shape
     _need(rng, "rng", torch.int64, (2,), dev)
-    _opt(row_ids, "row_ids", torch.int32, (x.shape[0],), dev)
+    _opt(row_ids, "row_ids", torch.int32, (T,), dev)
     out = torch.empty_like(x) if out is None else _need(out, "out", x.dtype, x.shape, dev)
-    _rc(_call(dev, N.load().moe_dropout, x.shape[0], x.shape[1], _DTYPES[x.dtype], float(p),
-              _p(x), _p(rng), int(first_row), _p(row_ids), _p(out)), "moe_dropout")
+    _rc(_call(dev, N.load().moe_dropout, T, H, _DTYPES[x.dtype], p, _p(x), _p(rng), first_row,
+              _p(row_ids), _p(out)), "moe_dropout")
     return out
 
 
@@ -705,10 +715,11 @@ def mx_grouped_ffn(cfg: Config, x, dest_row, offsets, w13, w2, w13_s=None, w2_s=
     w = _mx_experts(cfg, w13, w2, w13_s, w2_s, dev)
     y = torch.empty(T * K, H, dtype=torch.bfloat16, device=dev)
     y_s = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if Is else None
-    nbytes = workspace_bytes(cfg, N.MOE_STAGE_MX_FFN)
+    lib, ref = N.load(), ctypes.byref(cfg.c())
+    nbytes = lib.moe_workspace_bytes(ref, N.MOE_STAGE_MX_FFN)
     ws = _ws(nbytes, dev, ws)
     st = new_status(dev) if status is None and check else status
-    _rc(_call(dev, N.load().moe_mx_grouped_ffn, ctypes.byref(cfg.c()), _p(x), _p(dest_row),
+    _rc(_call(dev, lib.moe_mx_grouped_ffn, ref, _p(x), _p(dest_row),
               _p(offsets), *w, _p(y), _p(y_s), _p(st), _p(ws), nbytes), "moe_mx_grouped_ffn")
     if check:
         check_status(st)
@@ -730,7 +741,8 @@ def mx_forward(cfg: Config, x, w_router, w13, w2, logit_bias=None, sel_bias=None
     _opt(token_mask, "token_mask", torch.uint8, (T,), dev)
     out = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if out is None else out
     _need(out, "out", torch.bfloat16, (T, H), dev)
-    nbytes = workspace_bytes(cfg, N.MOE_STAGE_MX_FORWARD)
+    lib, ref = N.load(), ctypes.byref(cfg.c())
+    nbytes = lib.moe_workspace_bytes(ref, N.MOE_STAGE_MX_FORWARD)
     ws = _ws(nbytes, dev, ws)
     st = new_status(dev) if status is None else status
     b = {}
@@ -739,7 +751,7 @@ def mx_forward(cfg: Config, x, w_router, w13, w2, logit_bias=None, sel_bias=None
              "topk_ids": torch.empty(T, K, dtype=torch.int32, device=dev),
              "topk_w": torch.empty(T, K, dtype=torch.float32, device=dev),
              "offsets": torch.empty(E + 1, dtype=torch.int32, device=dev)}
-    _rc(_call(dev, N.load().moe_mx_forward, ctypes.byref(cfg.c()), _p(x), _p(w_router),
+    _rc(_call(dev, lib.moe_mx_forward, ref, _p(x), _p(w_router),
               _p(logit_bias), _p(sel_bias), _p(token_mask), *w, _p(out), _p(b.get("logits")),
               _p(b.get("topk_ids")), _p(b.get("topk_w")), _p(b.get("offsets")), _p(st), _p(ws),
               nbytes), "moe_mx_forward")
