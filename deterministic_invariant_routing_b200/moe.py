@@ -764,19 +764,32 @@ class MoELayer:
     """A layer holding its weights and a reusable workspace sized for up to max_T tokens.
 
     weights: dict with w_router, w13, w2 and optionally logit_bias, sel_bias, w13_s, w2_s
-    (the layout of include/moe.h)."""
+    (the layout of include/moe.h). Expert weights given as mx_weight() returned them make a
+    layer with 4-bit experts (mx_forward); quantized() makes one from a bf16 layer."""
 
     def __init__(self, cfg: Config, weights: dict, max_T: Optional[int] = None):
         self.cfg = cfg
         self.w = weights
         self.max_T = cfg.T if max_T is None else max_T
-        dev = weights["w13"].device
-        self.ws = _ws(workspace_bytes(cfg.with_T(self.max_T), N.MOE_STAGE_FORWARD), dev, None)
+        self.mx = not isinstance(weights["w13"], torch.Tensor)
+        dev = (weights["w13"][0] if self.mx else weights["w13"]).device
+        stage = N.MOE_STAGE_MX_FORWARD if self.mx else N.MOE_STAGE_FORWARD
+        self.ws = _ws(workspace_bytes(cfg.with_T(self.max_T), stage), dev, None)
         self.status = new_status(dev)
+
+    def quantized(self) -> "MoELayer":
+        """The same layer with its experts in the microscaled 4-bit format."""
+        if self.mx:
+            return self
+        w = {k: mx_weight(v) if k in ("w13", "w2", "w13_s", "w2_s") and v is not None else v
+             for k, v in self.w.items()}
+        return MoELayer(self.cfg, w, self.max_T)
 
     def forward_host(self, x_host, out_host=None, chunk: int = 6144, token_mask=None,
                      check=True):
         """The layer from pinned host memory to pinned host memory (see forward_host)."""
+        if self.mx:
+            raise MoeError("forward_host takes bf16 experts")
         T = x_host.shape[0]
         need = forward_host_workspace_bytes(self.cfg.with_T(T), chunk)
         if getattr(self, "_host_ws", None) is None or self._host_ws.numel() < need:
@@ -793,8 +806,70 @@ class MoELayer:
         if T > self.max_T:
             raise MoeError(f"{T} tokens > the layer's max_T {self.max_T}")
         w = self.w
+        if self.mx:
+            if stage_events is not None:
+                raise MoeError("stage events are recorded by a layer with bf16 experts")
+            return mx_forward(self.cfg.with_T(T), x, w["w_router"], w["w13"], w["w2"],
+                              logit_bias=w.get("logit_bias"), sel_bias=w.get("sel_bias"),
+                              token_mask=token_mask, w13_s=w.get("w13_s"), w2_s=w.get("w2_s"),
+                              out=out, ws=self.ws, status=self.status, keep=keep, check=check)
         return forward(self.cfg.with_T(T), x, w["w_router"], w["w13"], w["w2"],
                        logit_bias=w.get("logit_bias"), sel_bias=w.get("sel_bias"),
                        token_mask=token_mask, w13_s=w.get("w13_s"), w2_s=w.get("w2_s"),
                        out=out, ws=self.ws, status=self.status, keep=keep, check=check,
                        stage_events=stage_events)
+
+
+class MoEBlock:
+    """A layer and what joins its block to the next one:
+
+        y = layer(n),  r = residual_scale * x + branch_scale * gate * dropout(rmsnorm(y) * w_post)
+        n' = rmsnorm(r) * w_next
+
+    x is the residual stream, n its norm under this block's weight -- the n' that the block
+    before returned, or residual_norm(x, w_next=...)[1] before the first one. w_post, gate ([H])
+    and w_next are optional; p is the dropout probability of the training forward (a plain call
+    drops nothing). rng, first_row and row_ids: see dropout()."""
+
+    def __init__(self, layer: MoELayer, w_post=None, gate=None, w_next=None, eps: float = 1e-6,
+                 residual_scale: float = 1.0, branch_scale: float = 1.0, p: float = 0.0):
+        self.layer = layer
+        self.p = p
+        self.kw = dict(w_post=w_post, gate=gate, w_next=w_next, eps=eps,
+                       residual_scale=residual_scale, branch_scale=branch_scale)
+
+    def __call__(self, x, n, token_mask=None, check=True):
+        """(r, n') for serving, with bf16 or 4-bit experts."""
+        y = self.layer(n, token_mask=token_mask, check=check)
+        return residual_norm(x, y, **self.kw)
+
+    def forward_train(self, x, n, ws, rng=None, token_mask=None, first_row: int = 0, row_ids=None,
+                      check=True):
+        """(r, n', saved): the training forward, the layer's intermediates left in ws
+        (backward_workspace()), what backward() needs besides in saved."""
+        if self.layer.mx:
+            raise MoeError("training needs bf16 experts")
+        w, cfg = self.layer.w, self.layer.cfg.with_T(x.shape[0])
+        y, b = forward_train(cfg, n, w["w_router"], w["w13"], w["w2"], ws,
+                             logit_bias=w.get("logit_bias"), sel_bias=w.get("sel_bias"),
+                             token_mask=token_mask, w13_s=w.get("w13_s"), w2_s=w.get("w2_s"),
+                             check=check)
+        drop = dict(p=self.p, rng=rng, first_row=first_row, row_ids=row_ids)
+        r, n2 = residual_norm(x, y, **self.kw, **drop)
+        return r, n2, dict(n=n, y=y, r=r, routes=b, ws=ws, token_mask=token_mask, drop=drop)
+
+    def backward(self, saved: dict, dr=None, dn=None, check=True) -> dict:
+        """Gradients of sum(dr * r + dn * n'): {dx, dn} of the inputs -- the dr and dn of the
+        block before -- {dw_post, dgate, dw_next} as the block has them, and the layer's under
+        "layer" (see backward(); its dx is this dn)."""
+        w, cfg = self.layer.w, self.layer.cfg.with_T(saved["n"].shape[0])
+        g = residual_norm_backward(saved["r"], saved["y"], dr=dr, dn=dn, **self.kw,
+                                   **saved["drop"])
+        b = saved["routes"]
+        lay = backward(cfg, saved["n"], w["w_router"], w["w13"], w["w2"], b["logits"],
+                       b["topk_ids"], b["topk_w"], g.pop("dy"), token_mask=saved["token_mask"],
+                       w13_s=w.get("w13_s"), w2_s=w.get("w2_s"), ws=saved["ws"], saved=True,
+                       check=check)
+        g["dn"] = lay.pop("dx")
+        g["layer"] = lay
+        return g
