@@ -8,10 +8,15 @@
 // Every sum is fp32 in an order that depends on H alone (a thread's own vectors, a shuffle
 // tree in each warp, the warps in order): a token's row never depends on T or on its neighbours.
 //
-// All of it is bound by memory: 4 row passes forward (x, y in; r, n out), 6 backward (y, r, dr,
-// dn in; dx, dy out). A row stays in the registers of one block (one warp up to H = 512), so
-// nothing is read twice. The backward recomputes both norms' statistics and the dropout mask
-// from what it reads anyway: nothing but r and y is kept from the forward.
+// By its bytes it is bound by memory: 4 row passes forward (x, y in; r, n out), 6 backward (y,
+// r, dr, dn in; dx, dy out). A row stays in the registers of one block (one warp up to H = 512),
+// so nothing is read twice, and the backward recomputes both norms' statistics and the dropout
+// mask from what it reads anyway: nothing but r and y is kept from the forward. What bounds it
+// in fact is instructions: at 16-bit types a row pass leaves about 20 of them an element, and
+// the mask alone takes 8. Hence the packed fp32 arithmetic (F2), the kernels without branches for
+// the usual call, and the shuffles that add two values at once. Measured on B200:
+//   forward, 16384 x 2048 bf16, channel gate, dropout: 57 us (268 MB; 41 us at the copy's rate)
+//   backward, 8192 x 4096 bf16, the same:             121 us (403 MB; 61 us)
 //
 // Parameter gradients are column sums over tokens: block b of a grid whose size is a function
 // of (T, H) adds rows b, b + blocks, ... into its registers and writes one partial row; a second
@@ -599,9 +604,9 @@ __global__ void __launch_bounds__(32 * kSlices) param_grad_kernel(ReduceArgs a)
 }
 
 // out = keep ? x / probability : 0, each thread kVec vectors of 8, a block's width apart. A bf16
-// tensor moves 4 bytes an element and takes about 20 integer instructions for it (half of
-// Philox's are 32 x 32 -> 64 bit products): the arithmetic pipes bound it, at 30 % of the
-// memory rate short of them.
+// tensor moves 4 bytes an element and takes 15 instructions for it, 5 of them Philox's products
+// and xors: the integer pipes bound it (27.7 us for 16384 x 2048, 4.8 TB/s, 0.74 of the copy's
+// rate; 34 us with the keys formed per vector and a division per vector).
 constexpr int kVec = 4;
 
 template <int DT>

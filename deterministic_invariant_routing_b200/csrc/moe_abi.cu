@@ -504,6 +504,16 @@ MxFwdLayout mx_fwd_layout(const moe_cfg& c)
     return L;
 }
 
+// a call with nothing to do leaves clean status words
+int clear_status(int32_t* status, void* stream)
+{
+    if (status == nullptr) return MOE_OK;
+    const int rc = check_device();
+    if (rc != MOE_OK) return rc;
+    return cuda_rc(cudaMemsetAsync(status, 0, MOE_STATUS_WORDS * 4,
+                                   static_cast<cudaStream_t>(stream)));
+}
+
 // weights of 4-bit experts
 struct MxExperts {
     const uint8_t *w13, *w13_sc, *w2, *w2_sc, *w13_s, *w13_s_sc, *w2_s, *w2_s_sc;
@@ -1297,7 +1307,8 @@ MOE_API int moe_residual_norm(const moe_norm_cfg* cfg, const void* x, const void
     } else if (r == nullptr) {
         return MOE_ERR_ARG;
     }
-    if (x == nullptr || (cfg->p > 0.0 && rng == nullptr)) return MOE_ERR_ARG;
+    if (x == nullptr || (r != nullptr && r == n) || (cfg->p > 0.0 && rng == nullptr))
+        return MOE_ERR_ARG;
     if ((rc = check_aligned({x, y, w_post, w_next, r, n})) != MOE_OK) return rc;
     if (cfg->gate != MOE_GATE_TOKEN && !aligned16(gate)) return MOE_ERR_ARG;
     if ((rc = check_device()) != MOE_OK) return rc;
@@ -1337,7 +1348,7 @@ MOE_API int moe_residual_norm_backward(const moe_norm_cfg* cfg, const void* r, c
     if (y == nullptr && (w_post != nullptr || gate != nullptr || w_next == nullptr ||
                          cfg->residual_scale != 1.0f || cfg->p != 0.0))
         return MOE_ERR_ARG;
-    if (dx == nullptr || (dr == nullptr && dn == nullptr) || (w_next != nullptr && r == nullptr) ||
+    if (dx == nullptr || dx == dy || (dr == nullptr && dn == nullptr) || (w_next != nullptr && r == nullptr) ||
         (cfg->p > 0.0 && rng == nullptr))
         return MOE_ERR_ARG;
     if ((rc = check_aligned({r, y, w_post, w_next, dr, dn, dx, dy})) != MOE_OK) return rc;
@@ -1416,8 +1427,8 @@ MOE_API int moe_mx_grouped_gemm(int64_t rows, int32_t K, int32_t N, int32_t grou
     // rows of B are 32-bit coordinates
     if ((int64_t)groups * N >= ((int64_t)1 << 31) / 2) return MOE_ERR_SHAPE;
     if (offsets == nullptr && groups != 1) return MOE_ERR_ARG;
-    if (rows == 0) return MOE_OK;
     int rc;
+    if (rows == 0) return clear_status(status, stream);
     for (const void* p : std::initializer_list<const void*>{a_codes, a_scales, b_codes, b_scales, out})
         if (p == nullptr || !aligned16(p)) return MOE_ERR_ARG;
     if ((rc = check_device()) != MOE_OK) return rc;
@@ -1449,7 +1460,8 @@ MOE_API int moe_mx_grouped_ffn(const moe_cfg* cfg, const uint16_t* x, const int3
                                int32_t* status, void* ws, size_t ws_bytes, void* stream)
 {
     int rc = check_cfg(cfg);
-    if (rc != MOE_OK || cfg->T == 0) return rc;
+    if (rc != MOE_OK) return rc;
+    if (cfg->T == 0) return clear_status(status, stream);
     const MxExperts w{w13_codes, w13_scales, w2_codes, w2_scales,
                       w13_s_codes, w13_s_scales, w2_s_codes, w2_s_scales};
     if ((rc = check_mx_experts(*cfg, w)) != MOE_OK) return rc;
@@ -1477,7 +1489,8 @@ MOE_API int moe_mx_forward(const moe_cfg* cfg, const uint16_t* x, const uint16_t
                            void* ws, size_t ws_bytes, void* stream)
 {
     int rc = check_cfg(cfg);
-    if (rc != MOE_OK || cfg->T == 0) return rc;
+    if (rc != MOE_OK) return rc;
+    if (cfg->T == 0) return clear_status(status, stream);
     const moe_cfg& c = *cfg;
     const MxExperts w{w13_codes, w13_scales, w2_codes, w2_scales,
                       w13_s_codes, w13_s_scales, w2_s_codes, w2_s_scales};

@@ -437,7 +437,7 @@ typedef struct moe_norm_cfg {
  *          captured graph draws new masks when its owner changes them between replays.
  *  row_ids [T] int32 device or NULL: row t's mask is that of row row_ids[t] (taken as
  *          unsigned), instead of first_row + t.
- *  r       [T,H] out; may be x.   n [T,H] out; may be y.
+ *  r       [T,H] out; may be x.   n [T,H] out; may be y; not r.
  */
 MOE_API int moe_residual_norm(const moe_norm_cfg* cfg, const void* x, const void* y,
                               const void* w_post, const void* gate, const void* w_next,
@@ -452,7 +452,7 @@ MOE_API int moe_residual_norm(const moe_norm_cfg* cfg, const void* x, const void
  *  y, w_post, gate, w_next, rng, row_ids: the forward's.
  *  dr      [T,H] or NULL (r is used by the norm alone); dn [T,H], given exactly with w_next.
  *  dx      [T,H] out; may be dr.
- *  dy      [T,H] out (with y).
+ *  dy      [T,H] out (with y); not dx.
  *  dw_post [H], dw_next [H] fp32 out, given exactly with their weights.
  *  dgate   out, given exactly with gate: [H] or [T] fp32, or [T,H] of `dtype`.
  *  ws      moe_residual_norm_workspace_bytes(cfg) bytes.

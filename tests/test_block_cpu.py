@@ -94,6 +94,7 @@ def norm_cfg(**over):
 
 
 FAKE = ctypes.c_void_p(1 << 20)  # never dereferenced: validation fails first
+FAKE2 = ctypes.c_void_p(1 << 21)
 ODD = ctypes.c_void_p((1 << 20) + 8)
 BAD_CFGS = [dict(T=-1), dict(T=1 << 31), dict(H=0), dict(H=12), dict(H=16392), dict(first_row=-1),
             dict(first_row=(1 << 32) - 3), dict(dtype=3), dict(dtype=-1),
@@ -104,14 +105,14 @@ BAD_CFGS = [dict(T=-1), dict(T=1 << 31), dict(H=0), dict(H=12), dict(H=16392), d
 
 def fwd(lib, cfg, **over):
     p = dict(x=FAKE, y=FAKE, w_post=FAKE, gate=None, w_next=FAKE, rng=FAKE, row_ids=None, r=FAKE,
-             n=FAKE)
+             n=FAKE2)
     p.update(over)
     return lib.moe_residual_norm(ctypes.byref(cfg), *p.values(), None)
 
 
 def bwd(lib, cfg, ws_bytes=1 << 40, **over):
     p = dict(r=FAKE, y=FAKE, w_post=FAKE, gate=None, w_next=FAKE, rng=FAKE, row_ids=None, dr=FAKE,
-             dn=FAKE, dx=FAKE, dy=FAKE, dw_post=FAKE, dgate=None, dw_next=FAKE, ws=FAKE)
+             dn=FAKE, dx=FAKE, dy=FAKE2, dw_post=FAKE, dgate=None, dw_next=FAKE, ws=FAKE)
     p.update(over)
     return lib.moe_residual_norm_backward(ctypes.byref(cfg), *p.values(), ws_bytes, None)
 
@@ -131,11 +132,11 @@ def test_norm_pointer_combinations_rejected(lib):
     c = norm_cfg()
     for over in (dict(x=None), dict(r=None), dict(n=None), dict(w_next=None), dict(gate=FAKE),
                  dict(x=ODD), dict(y=ODD), dict(w_post=ODD), dict(w_next=ODD), dict(r=ODD),
-                 dict(n=ODD), dict(y=None), dict(y=None, r=None)):
+                 dict(n=ODD), dict(y=None), dict(y=None, r=None), dict(n=FAKE)):
         assert fwd(lib, c, **over) == N.MOE_ERR_ARG, over
     for over in (dict(r=None), dict(dx=None), dict(dy=None), dict(dn=None), dict(dw_next=None),
                  dict(dw_post=None), dict(w_post=None), dict(w_next=None), dict(gate=FAKE),
-                 dict(dgate=FAKE), dict(dx=ODD), dict(dr=ODD), dict(y=None)):
+                 dict(dgate=FAKE), dict(dx=ODD), dict(dr=ODD), dict(y=None), dict(dy=FAKE)):
         assert bwd(lib, c, **over) == N.MOE_ERR_ARG, over
     assert bwd(lib, c, w_next=None, dn=None, dw_next=None, dr=None) == N.MOE_ERR_ARG
     need = lib.moe_residual_norm_workspace_bytes(ctypes.byref(c))

@@ -223,6 +223,15 @@ def test_no_rows():
                         *moe.mx_weight(w), out=out)
     assert (out == 3).all()
     assert moe.mx_dequantize(*moe.mx_quantize(x[:0])).shape == (0, 128)
+    st = torch.ones(N.MOE_STATUS_WORDS, dtype=torch.int32, device=DEV)
+    moe.mx_grouped_gemm(*moe.mx_quantize(x[:0]), torch.zeros(3, dtype=torch.int32, device=DEV),
+                        *moe.mx_weight(w), status=st)  # what an earlier call left is cleared
+    cfg = moe.Config(T=0, H=128, E=2, K=1, I=128)
+    w2 = moe.mx_weight(w[:, :128].contiguous())
+    y, _ = moe.mx_grouped_ffn(cfg, x[:0], torch.zeros(0, 1, dtype=torch.int32, device=DEV),
+                              torch.zeros(3, dtype=torch.int32, device=DEV), moe.mx_weight(w), w2,
+                              status=st.fill_(1))
+    assert y.shape == (0, 128)
 
 
 # ------------------------------------------------------------------ the expert stage, the layer
