@@ -5,6 +5,9 @@ include/moe.h) with a thin torch binding.
     from deterministic_invariant_routing_b200 import moe
     out = moe.forward(moe.Config(T, H, E, K, I), x, w_router, w13, w2)
 
+Beside the layer: what joins its block to the next (``moe.residual_norm``, ``moe.dropout``,
+``moe.MoEBlock``, with gradients) and experts in the microscaled 4-bit format (``moe.mx_*``).
+
 Submodules: ``moe`` (the binding), ``build`` (nvcc build of the library), ``synthetic``
 (seeded inputs for tests and benchmarks). Importing the package loads nothing; the first
 binding call loads the library and raises if it is not built.
