@@ -43,10 +43,13 @@ struct NormArgs {
     float eps, inv_h, residual_scale, branch_scale, inv_keep;  // inv_h: 1 / H
 };
 
-// Sums K <= 4 values over a warp, the totals in every lane: each of the first shuffles adds two
-// values at once (a lane keeps one of them and gives the other away), so four values take 6
-// shuffles and 3 more to hand the totals out, not 20. The order of a value's sum is fixed.
-template <int K>
+// Sums K <= 4 values over a warp: each of the first shuffles adds two values at once (a lane keeps
+// one of them and gives the other away), so four values take 6 shuffles instead of 20. Value k's
+// total ends up in lane owner(k), and with ALL_LANES in every lane (a shuffle more per value).
+// The order of a value's sum is fixed.
+__device__ __forceinline__ int owner(int k) { return (k & 1) * 16 + (k >> 1) * 8; }
+
+template <int K, bool ALL_LANES>
 __device__ __forceinline__ void warp_sum(float (&v)[K])
 {
     constexpr uint32_t all = 0xffffffffu;
@@ -57,7 +60,7 @@ __device__ __forceinline__ void warp_sum(float (&v)[K])
     }
     const int lane = threadIdx.x & 31;
     const bool hi = lane & 16;
-    float a = v[0], b = v[K > 1 ? 1 : 0];
+    const float a = v[0], b = v[K > 1 ? 1 : 0];
     float p = (hi ? b : a) + __shfl_xor_sync(all, hi ? a : b, 16);  // sums of v0 | v1
     if (K > 2) {
         const float c = v[K > 2 ? 2 : 0], d = K > 3 ? v[K > 3 ? 3 : 0] : 0.0f;
@@ -69,10 +72,8 @@ __device__ __forceinline__ void warp_sum(float (&v)[K])
     }
 #pragma unroll
     for (int off = 4; off > 0; off >>= 1) p += __shfl_xor_sync(all, p, off);
-    v[0] = __shfl_sync(all, p, 0);
-    v[K > 1 ? 1 : 0] = __shfl_sync(all, p, 16);
-    if (K > 2) v[K > 2 ? 2 : 0] = __shfl_sync(all, p, 8);
-    if (K > 3) v[K > 3 ? 3 : 0] = __shfl_sync(all, p, 24);
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = ALL_LANES ? __shfl_sync(all, p, owner(k)) : p;
 }
 
 // Sums K values over a row's threads: within each warp, then over the warps' sums in shared
@@ -86,14 +87,14 @@ constexpr int kRed = 32;  // floats per value and half
 template <int K, int MAXT>
 __device__ __forceinline__ void row_sum(float (&v)[K], float* red, int& half)
 {
-    warp_sum<K>(v);
+    warp_sum<K, MAXT == 32>(v);
     if (MAXT == 32) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float* b = red + half * kRed * K;
     half ^= 1;
-    if (lane == 0)
 #pragma unroll
-        for (int k = 0; k < K; ++k) b[k * kRed + warp] = v[k];
+    for (int k = 0; k < K; ++k)
+        if (lane == owner(k)) b[k * kRed + warp] = v[k];
     __syncthreads();
     if (MAXT <= 256) {
 #pragma unroll
@@ -105,7 +106,7 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float* red, int& half)
     } else {
 #pragma unroll
         for (int k = 0; k < K; ++k) v[k] = b[k * kRed + lane];
-        warp_sum<K>(v);
+        warp_sum<K, true>(v);
     }
 }
 
@@ -140,8 +141,9 @@ __device__ __forceinline__ void drop2(const uint32_t (&w)[4], uint32_t threshold
 }
 
 // What a call has: kAny looks as it goes; kAll and kAllDrop are the usual call, with both norms
-// (backward: dr and room for the ring too) and fp32 parameters, without and with dropout. Bound
-// by instructions, the looking costs: a fifth of the backward's were branches and their constants.
+// (backward: dr and room for the ring too), fp32 parameters and rows that fill their threads,
+// without and with dropout. Bound by instructions, the looking costs: a fifth of the backward's
+// were branches and their constants.
 enum { kAny = 0, kAll = 1, kAllDrop = 2 };
 
 // one row per block of blockDim.x <= MAXT threads, or (MAXT = 32) one per warp, threadIdx.y the row
@@ -165,7 +167,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int v = tid + i * step;
-        if (v < a.nvec) {
+        if (ALL || v < a.nvec) {
             x[i].load(a.x, row + v);
             if (branch) y[i].load(a.y, row + v);
         }
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT)
             F2 acc = f2(0.0f);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                if (tid + i * step < a.nvec) {
+                if (ALL || tid + i * step < a.nvec) {
                     F2 q[4];
                     get2(y[i], q);
 #pragma unroll
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int v = tid + i * step;
-            if (v < a.nvec) {
+            if (ALL || v < a.nvec) {
                 F2 z[4], q[4];
                 get2(y[i], z);
 #pragma unroll
@@ -237,7 +239,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT)
     F2 acc = f2(0.0f);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        if (tid + i * step < a.nvec) {
+        if (ALL || tid + i * step < a.nvec) {
             F2 q[4];
             get2(x[i], q);  // the rounded r
 #pragma unroll
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int v = tid + i * step;
-        if (v < a.nvec) {
+        if (ALL || v < a.nvec) {
             F2 q[4], w[4];
             get2(x[i], q);
             load_param2<DT>(a.w_next, param_f32, v, w);
@@ -313,7 +315,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
     // with one vector a thread its weights and channel gate stay in registers
     constexpr bool KEEP = ALL && V == 1;
     F2 kn[4], kp[4], kg[4];
-    if (KEEP && tid < nvec) {
+    if (KEEP) {
         load_param2<DT>(a.w_next, true, tid, kn);
         load_param2<DT>(a.w_post, true, tid, kp);
         if (gate_mode == MOE_GATE_CHANNEL) load_param2<DT>(a.gate, true, tid, kg);
@@ -340,7 +342,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int v = tid + i * step;
-                if (v < nvec) {
+                if (ALL || v < nvec) {
 #pragma unroll
                     for (int h = 0; h < W16; ++h)
                         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
@@ -396,7 +398,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int v = tid + i * step;
-            if (v < nvec) {
+            if (ALL || v < nvec) {
                 F2 p[4], q[4], w[4];
                 if (next) {
                     get(at_r, a.r, row, i, p);
@@ -433,7 +435,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int v = tid + i * step;
-            if (v < nvec) {
+            if (ALL || v < nvec) {
                 F2 d[4], q[4];
                 if (has_dr) {
                     get(at_dr, a.dr, row, i, d);
@@ -528,7 +530,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int v = tid + i * step;
-                if (v < nvec) {
+                if (ALL || v < nvec) {
                     F2 y[4];
                     get(at_y, a.y, row, i, y);
 #pragma unroll
@@ -704,7 +706,8 @@ NormArgs base_args(const moe_norm_cfg& c)
 template <int DT, int V, int MAXT>
 cudaError_t norm_fwd_variant(const NormArgs& a, dim3 grid, dim3 block, cudaStream_t st)
 {
-    const bool all = a.w_post != nullptr && a.w_next != nullptr && a.param_f32;
+    const bool all = a.w_post != nullptr && a.w_next != nullptr && a.param_f32 &&
+                     a.nvec == V * (int)block.x;
     auto kernel = !all               ? residual_norm_kernel<DT, V, MAXT, kAny>
                   : a.threshold == 0 ? residual_norm_kernel<DT, V, MAXT, kAll>
                                      : residual_norm_kernel<DT, V, MAXT, kAllDrop>;
@@ -754,7 +757,7 @@ cudaError_t norm_bwd_variant(const NormArgs& a, BwdRing g, dim3 grid, dim3 block
     if (g.stages > 4) g.stages = 4;
     const size_t smem = g.stages * stage;
     if (a.w_post == nullptr || a.w_next == nullptr || a.dr == nullptr || !a.param_f32 ||
-        g.stages == 0)
+        a.nvec != V * (int)block.x || g.stages == 0)
         return norm_bwd_launch<DT, V, MAXT, kAny>(a, g, grid, block, smem, st);
     return a.threshold != 0
                ? norm_bwd_launch<DT, V, MAXT, kAllDrop>(a, g, grid, block, smem, st)

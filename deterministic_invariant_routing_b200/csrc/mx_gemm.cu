@@ -347,11 +347,12 @@ __global__ void __launch_bounds__(kXThreads, 1)
             const int b1 = kGlu ? b0 + args.half / 128 : b0 + 1;  // 128-row tiles of B
             const int brow = (leader ? b0 : b1) * 128;
             // a whole tile's rows come in one box; of a partial one only the 32-row boxes with
-            // rows of the group (decode-sized groups read few rows)
+            // rows of the group are read (decode-sized groups read few rows), the others come
+            // from past the tensor's end, as zeros: 24594 rows over 256 experts, most of a
+            // tile's rows padding, take 324 us in a loop at the power cap with zeros there and
+            // 334 with whatever the stage held
             const uint32_t mine = (uint32_t)uniform((int)mx_boxes(ti, rank));
-            const uint32_t other = (uint32_t)uniform((int)mx_boxes(ti, rank ^ 1u));
-            const uint32_t bytes = 2 * (kXB + kXSA + kXSB) +
-                                   kXBox * (uint32_t)(__popc(mine) + __popc(other));
+            const int past = (int)args.rows;
             const int sa = (arow >> 7) * kc, sb0 = b0 * kc, sb1 = b1 * kc;
             bool ok = true;
             for (int kb = 0; kb < args.k_blocks; ++kb) {
@@ -361,15 +362,14 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 }
                 const uint32_t fb = fb0 + 8u * (uint32_t)stage, ss = (uint32_t)stage;
                 if (elect_one()) {
-                    if (leader) mbar_expect_tx(full_bar(stage), bytes);
+                    if (leader) mbar_expect_tx(full_bar(stage), 2 * kXStage);
                     if (mine == 15u) {
                         tma_load_2d_pair(sA0 + ss * kXA, &tmA, kb * (XK / 2), arow, fb);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            if (mine >> j & 1u)
-                                tma_load_2d_pair(sA0 + ss * kXA + j * kXBox, &tmA32, kb * (XK / 2),
-                                                 arow + 32 * j, fb);
+                            tma_load_2d_pair(sA0 + ss * kXA + j * kXBox, &tmA32, kb * (XK / 2),
+                                             mine >> j & 1u ? arow + 32 * j : past, fb);
                     }
                     tma_load_2d_pair(sB0 + ss * kXB, &tmB, kb * (XK / 2), brow, fb);
                     tma_load_2d_pair(sSA0 + ss * kXSA, &tmSA, 0, sa + 2 * kb, fb);

@@ -297,38 +297,38 @@ def _norm_setup(x, y, w_post, gate, w_next, eps, residual_scale, branch_scale, p
     """The checks that residual_norm and its backward share; their configuration."""
     shape, dt, dev = x.shape, x.dtype, x.device
     T, H = shape
+    code = _DTYPES[dt]
     if y is not None:
         _need(y, "y", dt, shape, dev)
     elif w_post is not None or gate is not None or p or w_next is None or residual_scale != 1.0:
         raise MoeError("without y there is only the norm: w_next is required, and w_post, gate, "
                        "p and residual_scale do not apply")
-    mode, small_gate = N.MOE_GATE_NONE, None
+    mode, small = N.MOE_GATE_NONE, None
     if gate is not None:
-        g = tuple(gate.shape)
+        g = gate.shape
         if g == (H,):
-            mode, small_gate = N.MOE_GATE_CHANNEL, gate
+            mode, small = N.MOE_GATE_CHANNEL, gate
         elif g == (T, 1):
-            mode, small_gate = N.MOE_GATE_TOKEN, gate
-        elif g == (T, H):
+            mode, small = N.MOE_GATE_TOKEN, gate
+        elif g == shape:
             mode = N.MOE_GATE_FULL
             _need(gate, "gate", dt, shape, dev)
         else:
-            raise MoeError(f"gate: shape {g}, expected ({H},), ({T}, 1) or ({T}, {H})")
-    pd = None
-    for t, name, want in ((w_post, "w_post", (H,)), (w_next, "w_next", (H,)),
-                          (small_gate, "gate", None)):
-        if t is None:
-            continue
-        if pd is None:
-            pd = t.dtype
-            if pd is not torch.float32 and pd is not dt:
-                raise MoeError(f"{name}: dtype {pd}, expected torch.float32 or {dt}")
-        _need(t, name, pd, t.shape if want is None else want, dev)
+            raise MoeError(f"gate: shape {tuple(g)}, expected ({H},), ({T}, 1) or ({T}, {H})")
+    first = w_post if w_post is not None else w_next if w_next is not None else small
+    pd = torch.float32 if first is None else first.dtype
+    if pd is not torch.float32 and pd is not dt:
+        raise MoeError(f"parameters: dtype {pd}, expected torch.float32 or {dt}")
+    if w_post is not None:
+        _need(w_post, "w_post", pd, (H,), dev)
+    if w_next is not None:
+        _need(w_next, "w_next", pd, (H,), dev)
+    if small is not None:
+        _need(small, "gate", pd, small.shape, dev)
     if p:
         _need(rng, "rng", torch.int64, (2,), dev)
     if row_ids is not None:
         _need(row_ids, "row_ids", torch.int32, (T,), dev)
-    code = _DTYPES[dt]
     return N.MoeNormCfg(T, first_row, p, H, code, code if pd is dt else N.MOE_F32, mode, eps,
                         residual_scale, branch_scale)
 
@@ -611,7 +611,8 @@ def mx_quantize(x, tiled: bool = True):
     _act(x, "x")
     dev, (R, K) = x.device, x.shape
     codes = torch.empty(R, K // 2, dtype=torch.uint8, device=dev)
-    scales = torch.empty(_mx_tiles(R, K) if tiled else (R, K // 32), dtype=torch.uint8, device=dev)
+    scales = torch.empty(-(-R // 128), -(-K // 128), 512, dtype=torch.uint8, device=dev) if tiled \
+        else torch.empty(R, K // 32, dtype=torch.uint8, device=dev)
     _rc(_call(dev, N.load().moe_mx_quantize, R, K, _DTYPES[x.dtype], int(bool(tiled)), _p(x),
               _p(codes), _p(scales)), "moe_mx_quantize")
     return codes, scales
@@ -679,9 +680,9 @@ def mx_grouped_gemm(codes, scales, offsets, w_codes, w_scales, swiglu: bool = Fa
     _need(scales, "scales", torch.uint8, _mx_tiles(R, K), dev)
     _need(offsets, "offsets", torch.int32, (E + 1,), dev)
     _mx_need((w_codes, w_scales), "w", (E, n, K), dev)
-    shape = (R, n // 2 if swiglu else n)
-    out = torch.empty(shape, dtype=torch.bfloat16, device=dev) if out is None else out
-    _need(out, "out", torch.bfloat16, shape, dev)
+    cols = n // 2 if swiglu else n
+    out = torch.empty(R, cols, dtype=torch.bfloat16, device=dev) if out is None else \
+        _need(out, "out", torch.bfloat16, (R, cols), dev)
     st = new_status(dev) if status is None and check else status
     _rc(_call(dev, N.load().moe_mx_grouped_gemm, R, K, n, E, int(bool(swiglu)), _p(codes),
               _p(scales), _p(offsets), _p(w_codes), _p(w_scales), _p(out), _p(st)),
