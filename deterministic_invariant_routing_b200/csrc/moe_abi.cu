@@ -44,13 +44,17 @@ int resident_blocks(const void* kernel, int threads, size_t smem)
 
 bool device_is_sm100()
 {
+    static int8_t cached[64] = {};  // 0: not asked yet, 1: yes, -1: no
     int dev = 0, major = 0, minor = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev >= 0 && dev < 64 && cached[dev] != 0) return cached[dev] > 0;
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
         return false;
     if (cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
         return false;
-    return major == 10 && minor == 0;
+    const bool yes = major == 10 && minor == 0;
+    if (dev >= 0 && dev < 64) cached[dev] = yes ? 1 : -1;
+    return yes;
 }
 
 namespace {

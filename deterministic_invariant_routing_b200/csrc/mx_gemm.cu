@@ -685,16 +685,20 @@ cudaError_t launch_mode(const MxProblem& p, cudaStream_t st)
     }
     const bool glu = MODE != MX_BF16;
     const int b_rows = glu ? 2 * p.n : p.n;
+    // (encoding a map takes half a microsecond of the call; those that this many rows cannot
+    // use are stand-ins: a row in each of four 32-row boxes takes 66 rows, a store tile 32)
     CUtensorMap ma, ma32, mb, msa, ms, mo;
-    if (!make_codes_map(&ma, p.a, p.rows, p.k, XH)) return cudaErrorInvalidValue;
     if (!make_codes_map(&ma32, p.a, p.rows, p.k, 32)) return cudaErrorInvalidValue;
+    if (!make_codes_map(&mb, p.b, (int64_t)p.groups * b_rows, p.k, XH)) return cudaErrorInvalidValue;
     if (!make_scale_map(&msa, p.a_scales, (p.rows + 127) / 128 * (p.k / 128)))
         return cudaErrorInvalidValue;
-    if (!make_codes_map(&mb, p.b, (int64_t)p.groups * b_rows, p.k, XH)) return cudaErrorInvalidValue;
     if (!make_scale_map(&ms, p.b_scales, (int64_t)p.groups * (b_rows / 128) * (p.k / 128)))
         return cudaErrorInvalidValue;
-    if (MODE == MX_SWIGLU_QUANT) mo = ma;  // stored from registers: the map is not used
-    else if (!make_out_map(&mo, p.out, p.rows, p.n)) return cudaErrorInvalidValue;
+    ma = ma32;
+    if (p.rows >= 66 && !make_codes_map(&ma, p.a, p.rows, p.k, XH)) return cudaErrorInvalidValue;
+    mo = ma32;  // quantised outputs are stored from registers
+    if (MODE != MX_SWIGLU_QUANT && p.rows >= 32 && !make_out_map(&mo, p.out, p.rows, p.n))
+        return cudaErrorInvalidValue;
     MxArgs a{};
     a.k = p.k;
     a.k_blocks = (p.k + XK - 1) / XK;

@@ -654,14 +654,12 @@ def mx_dequantize(codes, scales, dtype=torch.bfloat16):
     return out
 
 
-def _mx_need(w, name, shape, dev):
-    """4-bit weights (codes, tiled scales) for matrices of this shape [..., N, K]."""
+def _mx_need(w, name, n, k, dev, lead=()):
+    """4-bit weights (codes, tiled scales) of matrices [n, k], lead = (how many,) or ()."""
     if w is None or len(w) != 2:
         raise MoeError(f"{name}: (codes, scales) of mx_weight() are expected")
-    *lead, n, k = shape
-    _need(w[0], f"{name} codes", torch.uint8, (*lead, n, k // 2), dev)
-    _need(w[1], f"{name} scales", torch.uint8, (*lead, n // 128, k // 128, 512), dev)
-    return w
+    _need(w[0], f"{name} codes", torch.uint8, lead + (n, k // 2), dev)
+    _need(w[1], f"{name} scales", torch.uint8, lead + (n // 128, k // 128, 512), dev)
 
 
 def mx_grouped_gemm(codes, scales, offsets, w_codes, w_scales, swiglu: bool = False, out=None,
@@ -679,7 +677,7 @@ def mx_grouped_gemm(codes, scales, offsets, w_codes, w_scales, swiglu: bool = Fa
     _need(codes, "codes", torch.uint8, (R, K // 2), dev)
     _need(scales, "scales", torch.uint8, _mx_tiles(R, K), dev)
     _need(offsets, "offsets", torch.int32, (E + 1,), dev)
-    _mx_need((w_codes, w_scales), "w", (E, n, K), dev)
+    _mx_need((w_codes, w_scales), "w", n, K, dev, (E,))
     cols = n // 2 if swiglu else n
     out = torch.empty(R, cols, dtype=torch.bfloat16, device=dev) if out is None else \
         _need(out, "out", torch.bfloat16, (R, cols), dev)
@@ -693,14 +691,16 @@ def mx_grouped_gemm(codes, scales, offsets, w_codes, w_scales, swiglu: bool = Fa
 
 
 def _mx_experts(cfg, w13, w2, w13_s, w2_s, dev):
-    H, E, I, Is = cfg.H, cfg.E, cfg.I, cfg.I_shared
-    _mx_need(w13, "w13", (E, 2 * I, H), dev)
-    _mx_need(w2, "w2", (E, H, I), dev)
+    """The pointers of a layer's 4-bit expert weights, checked."""
+    H, I, Is, E = cfg.H, cfg.I, cfg.I_shared, (cfg.E,)
+    _mx_need(w13, "w13", 2 * I, H, dev, E)
+    _mx_need(w2, "w2", H, I, dev, E)
+    p = (w13[0].data_ptr(), w13[1].data_ptr(), w2[0].data_ptr(), w2[1].data_ptr())
     if not Is:
-        return [*map(_p, (*w13, *w2))] + [None] * 4
-    _mx_need(w13_s, "w13_s", (2 * Is, H), dev)
-    _mx_need(w2_s, "w2_s", (H, Is), dev)
-    return [*map(_p, (*w13, *w2, *w13_s, *w2_s))]
+        return p + (None, None, None, None)
+    _mx_need(w13_s, "w13_s", 2 * Is, H, dev)
+    _mx_need(w2_s, "w2_s", H, Is, dev)
+    return p + (w13_s[0].data_ptr(), w13_s[1].data_ptr(), w2_s[0].data_ptr(), w2_s[1].data_ptr())
 
 
 def mx_grouped_ffn(cfg: Config, x, dest_row, offsets, w13, w2, w13_s=None, w2_s=None, ws=None,

@@ -145,6 +145,18 @@ def test_rows_outside_the_groups_are_left(swiglu):
     check_product(out, x, w, off, swiglu, 256)
 
 
+@pytest.mark.parametrize("start,n", [(0, 31), (1, 31), (0, 32), (31, 65), (31, 66), (30, 67),
+                                     (62, 66), (0, 97), (0, 98), (31, 97), (127, 1), (127, 2)])
+def test_few_rows_at_every_place_of_a_tile(start, n):
+    """Calls of so few rows that whole boxes and store tiles just do or do not occur."""
+    x, w, off = make_product([n], 256, 384, seed=n, start=start)
+    for swiglu in (False, True):
+        out = moe.mx_grouped_gemm(*moe.mx_quantize(x),
+                                  torch.tensor(off, dtype=torch.int32, device=DEV),
+                                  *moe.mx_weight(w), swiglu=swiglu)
+        check_product(out, x, w, off, swiglu, 384)
+
+
 def test_many_tiles_a_cluster():
     """More tiles than clusters take at once, uneven groups: every role keeps its phases."""
     g = torch.randperm(64, generator=torch.Generator().manual_seed(1)).tolist()
