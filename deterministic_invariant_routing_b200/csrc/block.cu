@@ -320,21 +320,51 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
         load_param2<DT>(a.w_post, true, tid, kp);
         if (gate_mode == MOE_GATE_CHANNEL) load_param2<DT>(a.gate, true, tid, kg);
     }
-    auto param = [&](const void* p, const F2 (&kept)[4], int v, F2 (&w)[4]) {
+    // (this thread's place in the ring: 16 bytes per thread, arrays and vectors `lane16` apart)
+    // with two, in its own slots of shared memory behind the ring (read from memory they come
+    // from L2: beside the ring, L1 holds less than a row's weights)
+    constexpr bool SLOTS = ALL && V == 2 && MAXT != 1024;
+    const uint32_t lane16 = (uint32_t)threads * 16u;
+    const uint32_t ring0 = (uint32_t)__cvta_generic_to_shared(ring) + (uint32_t)lin * 16u;
+    const uint32_t stage_bytes = (uint32_t)(g.arrays * V * W16) * lane16;
+    const uint32_t slots0 = ring0 + (uint32_t)g.stages * stage_bytes;
+    auto param_slot = [&](int which, int i, int h) {
+        return slots0 + (uint32_t)((which * V + i) * 2 + h) * lane16;
+    };
+    if (SLOTS) {
+        auto stage_in = [&](int which, const void* p) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(
+                                     param_slot(which, i, h)),
+                                 "l"(static_cast<const uint4*>(p) + 2 * (tid + i * step) + h)
+                                 : "memory");
+        };
+        stage_in(0, a.w_next);
+        stage_in(1, a.w_post);
+        if (gate_mode == MOE_GATE_CHANNEL) stage_in(2, a.gate);
+        asm volatile("cp.async.commit_group;" ::: "memory");  // older than every row's group
+    }
+    auto param = [&](const void* p, const F2 (&kept)[4], int which, int i, F2 (&w)[4]) {
         if (KEEP) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = kept[e];
+        } else if (SLOTS) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
+                             : "=l"(w[2 * h].v), "=l"(w[2 * h + 1].v)
+                             : "r"(param_slot(which, i, h))
+                             : "memory");
         } else {
-            load_param2<DT>(p, param_f32, v, w);
+            load_param2<DT>(p, param_f32, tid + i * step, w);
         }
     };
     Philox ph;
     if (drop) ph = philox_load(a.rng);
 
-    // this thread's place in the ring: 16 bytes per thread, arrays and vectors `lane16` apart
-    const uint32_t lane16 = (uint32_t)threads * 16u;
-    const uint32_t ring0 = (uint32_t)__cvta_generic_to_shared(ring) + (uint32_t)lin * 16u;
-    const uint32_t stage_bytes = (uint32_t)(g.arrays * V * W16) * lane16;
     auto fetch = [&](uint32_t at, int64_t t) {
         auto one = [&](int array, const void* p) {
             if (array < 0) return;
@@ -403,7 +433,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
                 if (next) {
                     get(at_r, a.r, row, i, p);
                     get(at_dn, a.dn, row, i, q);
-                    param(a.w_next, kn, v, w);
+                    param(a.w_next, kn, 0, i, w);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         rr = fma2(p[e], p[e], rr);
@@ -455,7 +485,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
                         get(at_r, a.r, row, i, p);
                         get(at_dn, a.dn, row, i, q);
                     }
-                    param(a.w_next, kn, v, w);
+                    param(a.w_next, kn, 0, i, w);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const F2 k = mul2(q[e], s2x);
@@ -479,7 +509,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
                         d[e] = mul2(d[e], bscale);
                         yu[e] = mul2(yu[e], u2x);
                     }
-                    if (post) param(a.w_post, kp, v, w);
+                    if (post) param(a.w_post, kp, 1, i, w);
                     if (drop) drop2(bitsw, threshold, d);
                     if (gate_mode != MOE_GATE_NONE) {
                         // b z: the factor 1 / P(keep) of z is already in d, dropped ones are 0
@@ -494,7 +524,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
                             set2(o, z);
                             o.store(a.dgate, row + v);
                         } else if (gate_mode == MOE_GATE_CHANNEL) {
-                            param(a.gate, kg, v, q);
+                            param(a.gate, kg, 2, i, q);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) gg[i][e] = fma2(d[e], z[e], gg[i][e]);
                         } else {
@@ -663,11 +693,11 @@ RowShape row_shape(int nvec)
 
 constexpr int kWarpRows = 4;  // rows of a block in the one-warp form
 
-// the backward: one vector a thread (24 sums and 24 weights in registers) up to H = 4096
+// the backward: one vector a thread (24 sums and 24 weights in registers) up to H = 2048
 RowShape bwd_shape(int nvec)
 {
     if (nvec <= 32) return {true, 1, 32};
-    if (nvec <= 512) return {false, 1, (nvec + 31) / 32 * 32};
+    if (nvec <= 256) return {false, 1, (nvec + 31) / 32 * 32};
     return {false, 2, ((nvec + 1) / 2 + 31) / 32 * 32};
 }
 
@@ -740,7 +770,8 @@ cudaError_t norm_bwd_launch(const NormArgs& a, const BwdRing& g, dim3 grid, dim3
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     static bool attr_set[64] = {};
     if (!attr_set[dev]) {
-        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 226000);
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   233472 - 1024 - 768);
         if (err != cudaSuccess) return err;
         attr_set[dev] = true;
     }
@@ -753,12 +784,22 @@ cudaError_t norm_bwd_variant(const NormArgs& a, BwdRing g, dim3 grid, dim3 block
     const int threads = (int)(block.x * block.y);
     const int per_sm = threads <= 512 ? 512 / threads : 1;
     const size_t stage = (size_t)g.arrays * V * (DT == MOE_F32 ? 32 : 16) * threads;
-    g.stages = (int32_t)(225000 / per_sm / (stage > 0 ? stage : 1));
-    if (g.stages > 4) g.stages = 4;
-    const size_t smem = g.stages * stage;
-    if (a.w_post == nullptr || a.w_next == nullptr || a.dr == nullptr || !a.param_f32 ||
-        a.nvec != V * (int)block.x || g.stages == 0)
-        return norm_bwd_launch<DT, V, MAXT, kAny>(a, g, grid, block, smem, st);
+    // an SM's 228 KB, less a block's kilobyte and its static part, for per_sm blocks
+    const size_t room = 233472 / per_sm - 1024 - 768;
+    // the weights' slots of kAll and kAllDrop (V = 2)
+    const size_t slots = V == 2 && MAXT != 1024
+                             ? (size_t)(a.gate_mode == MOE_GATE_CHANNEL ? 3 : 2) * V * 32 * threads
+                             : 0;
+    auto stages_in = [&](size_t bytes) {
+        const size_t n = stage > 0 ? bytes / stage : 0;
+        return (int32_t)(n > 4 ? 4 : n);
+    };
+    g.stages = room > slots ? stages_in(room - slots) : 0;
+    const bool all = a.w_post != nullptr && a.w_next != nullptr && a.dr != nullptr && a.param_f32 &&
+                     a.nvec == V * (int)block.x && g.stages > 0;
+    if (!all) g.stages = stages_in(room);
+    const size_t smem = g.stages * stage + (all ? slots : 0);
+    if (!all) return norm_bwd_launch<DT, V, MAXT, kAny>(a, g, grid, block, smem, st);
     return a.threshold != 0
                ? norm_bwd_launch<DT, V, MAXT, kAllDrop>(a, g, grid, block, smem, st)
                : norm_bwd_launch<DT, V, MAXT, kAll>(a, g, grid, block, smem, st);
@@ -779,9 +820,8 @@ cudaError_t norm_bwd(const NormArgs& a, int64_t groups, cudaStream_t st)
         return norm_bwd_variant<DT, 1, 32>(a, g, dim3((unsigned)(groups / kWarpRows)),
                                            dim3(32, kWarpRows), st);
     const dim3 grid((unsigned)groups), block(s.threads);
-    if (s.V == 1)
-        return s.threads <= 256 ? norm_bwd_variant<DT, 1, 256>(a, g, grid, block, st)
-                                : norm_bwd_variant<DT, 1, 512>(a, g, grid, block, st);
+    if (s.V == 1) return norm_bwd_variant<DT, 1, 256>(a, g, grid, block, st);
+    if (s.threads <= 256) return norm_bwd_variant<DT, 2, 256>(a, g, grid, block, st);
     if (s.threads <= 512) return norm_bwd_variant<DT, 2, 512>(a, g, grid, block, st);
     return norm_bwd_variant<DT, 2, 1024>(a, g, grid, block, st);
 }
