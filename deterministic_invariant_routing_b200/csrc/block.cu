@@ -693,20 +693,23 @@ RowShape row_shape(int nvec)
 
 constexpr int kWarpRows = 4;  // rows of a block in the one-warp form
 
-// the backward: one vector a thread (24 sums and 24 weights in registers) up to H = 2048
-RowShape bwd_shape(int nvec)
+// The backward: one vector a thread (its 24 sums and 24 weights in registers) up to H = 512, or in
+// fp32, where the ring leaves no room for weights in shared memory, up to H = 2048; two beyond
+// that. 16384 x 2048 with dropout and a channel gate, one vector against two: bf16 112 and 104
+// us, fp32 218 and 296.
+RowShape bwd_shape(int nvec, int dtype)
 {
     if (nvec <= 32) return {true, 1, 32};
-    if (nvec <= 256) return {false, 1, (nvec + 31) / 32 * 32};
+    if (nvec <= (dtype == MOE_F32 ? 256 : 64)) return {false, 1, (nvec + 31) / 32 * 32};
     return {false, 2, ((nvec + 1) / 2 + 31) / 32 * 32};
 }
 
-// row groups of the backward: a function of (T, H) alone, so that the order of the parameter
-// sums does not depend on the device (about 512 threads for each of a B200's 148 SMs, at least
-// two rows a group)
-int64_t bwd_groups(int64_t T, int32_t H)
+// row groups of the backward: a function of T, H and the type alone, so that the order of the
+// parameter sums does not depend on the device (about 512 threads for each of a B200's 148 SMs,
+// at least two rows a group)
+int64_t bwd_groups(int64_t T, int32_t H, int dtype)
 {
-    const RowShape s = bwd_shape(H / 8);
+    const RowShape s = bwd_shape(H / 8, dtype);
     int64_t per_sm = 512 / s.threads;
     if (per_sm < 1) per_sm = 1;
     int64_t g = 148 * per_sm;
@@ -815,7 +818,7 @@ cudaError_t norm_bwd(const NormArgs& a, int64_t groups, cudaStream_t st)
     g.i_dr = take(a.dr != nullptr);
     g.i_y = take(a.y != nullptr);
     g.i_gate = take(a.gate_mode == MOE_GATE_FULL);
-    const RowShape s = bwd_shape(a.nvec);
+    const RowShape s = bwd_shape(a.nvec, DT);
     if (s.one_warp)
         return norm_bwd_variant<DT, 1, 32>(a, g, dim3((unsigned)(groups / kWarpRows)),
                                            dim3(32, kWarpRows), st);
@@ -842,7 +845,7 @@ float dropout_scale(uint32_t threshold)
 
 size_t residual_norm_bwd_ws_bytes(const moe_norm_cfg& c)
 {
-    return (size_t)bwd_groups(c.T, c.H) * 3 * (size_t)c.H * sizeof(float);
+    return (size_t)bwd_groups(c.T, c.H, c.dtype) * 3 * (size_t)c.H * sizeof(float);
 }
 
 cudaError_t launch_residual_norm(const moe_norm_cfg& c, const void* x, const void* y,
@@ -873,7 +876,7 @@ cudaError_t launch_residual_norm_bwd(const moe_norm_cfg& c, const void* r, const
                                      const void* dn, void* dx, void* dy, float* dw_post,
                                      void* dgate, float* dw_next, void* ws, cudaStream_t st)
 {
-    const int64_t groups = bwd_groups(c.T, c.H);
+    const int64_t groups = bwd_groups(c.T, c.H, c.dtype);
     NormArgs a = base_args(c);
     a.r = const_cast<void*>(r);
     a.y = y;

@@ -456,7 +456,7 @@ MOE_API int moe_residual_norm(const moe_norm_cfg* cfg, const void* x, const void
  *  dw_post [H], dw_next [H] fp32 out, given exactly with their weights.
  *  dgate   out, given exactly with gate: [H] or [T] fp32, or [T,H] of `dtype`.
  *  ws      moe_residual_norm_workspace_bytes(cfg) bytes.
- * Parameter gradients are summed over tokens in fp32 in an order that is a function of (T, H):
+ * Parameter gradients are summed over tokens in fp32 in an order that is a function of (T, H, dtype):
  * bitwise repeatable. T == 0 gives zeros (per-token pointers may be NULL then, here and in
  * the forward). dx and dy of a row depend on that row alone.
  */
