@@ -11,6 +11,7 @@ import threading
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "libmoe_b200.so")
+BINDING_PATH = os.path.join(_PKG, "_lib", "moe_binding.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "moe.h")
 
 MOE_OK = 0
@@ -128,6 +129,31 @@ def load():
                 f.argtypes = args
             _lib = lib
     return _lib
+
+
+_binding = None
+
+
+def load_binding(error):
+    """The native part of the binding (csrc/binding.cpp), raising `error` for what it refuses."""
+    global _binding
+    load()
+    with _lock:
+        if _binding is None:
+            if not os.path.exists(BINDING_PATH):
+                raise RuntimeError(
+                    f"moe_binding.so is not built ({BINDING_PATH}); run "
+                    "`python -m deterministic_invariant_routing_b200.build` (needs nvcc and g++)")
+            import importlib.machinery
+            import importlib.util
+            loader = importlib.machinery.ExtensionFileLoader("moe_binding", BINDING_PATH)
+            spec = importlib.util.spec_from_file_location("moe_binding", BINDING_PATH,
+                                                          loader=loader)
+            m = importlib.util.module_from_spec(spec)
+            loader.exec_module(m)
+            m.init(error)
+            _binding = m
+    return _binding
 
 
 def status_string(code: int) -> str:

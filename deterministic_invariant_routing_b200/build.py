@@ -1,4 +1,5 @@
-"""Build libmoe_b200.so from csrc/*.cu with nvcc for sm_100a (B200), in-tree.
+"""Build libmoe_b200.so from csrc/*.cu with nvcc for sm_100a (B200), and the native part of the
+binding, moe_binding.so, from csrc/binding.cpp with g++ against torch's headers, in-tree.
 
 Usage: python -m deterministic_invariant_routing_b200.build [--force] [--verbose-ptxas]
 """
@@ -18,6 +19,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libmoe_b200.so")
 HEADER = os.path.join(ROOT, "include", "moe.h")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING_PATH = os.path.join(LIB_DIR, "moe_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -47,6 +50,38 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def _binding_up_to_date() -> bool:
+    if not os.path.exists(BINDING_PATH):
+        return False
+    t = os.path.getmtime(BINDING_PATH)
+    return all(os.path.getmtime(p) <= t for p in (BINDING_SRC, HEADER))
+
+
+def _build_binding() -> None:
+    import sysconfig
+
+    import torch
+    cxx = shutil.which("g++")
+    if cxx is None:
+        raise RuntimeError("g++ not found: it is needed to build moe_binding.so")
+    tmp = BINDING_PATH + f".{os.getpid()}.tmp"
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    inc = [os.path.join(os.path.dirname(torch.__file__), "include"),
+           os.path.join(os.path.dirname(torch.__file__), "include", "torch", "csrc", "api",
+                        "include"),
+           sysconfig.get_paths()["include"], cuda, os.path.join(ROOT, "include")]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f for d in inc for f in ("-isystem", d)], BINDING_SRC, "-o", tmp, "-L", LIB_DIR,
+           "-l:libmoe_b200.so", "-L", libs, "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10",
+           "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_PATH)
+
+
 def _compile(src: str, extra) -> str:
     obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
     cmd = [nvcc(), *NVCC_FLAGS, *extra, "-c", src, "-o", obj]
@@ -59,8 +94,11 @@ def _compile(src: str, extra) -> str:
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile every kernel for sm_100a and link the shared library. Returns its path."""
+    """Compile every kernel for sm_100a and link the shared library, then the binding. Returns the
+    library's path."""
     if not force and not verbose_ptxas and up_to_date():
+        if not _binding_up_to_date():
+            _build_binding()
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
@@ -74,6 +112,8 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    if force or not _binding_up_to_date():
+        _build_binding()
     return LIB_PATH
 
 

@@ -1,4 +1,5 @@
-"""Python binding of libmoe_b200: torch tensors in, the C ABI's calls out.
+"""Python binding of libmoe_b200: torch tensors in, the C ABI's calls out (through ctypes for the
+layer's calls, through csrc/binding.cpp for the small ones around it).
 
 Argument marshalling only -- shapes, dtypes and devices are checked, buffers are
 allocated with torch (device memory is torch's), and every step of the layer runs in
@@ -273,16 +274,14 @@ def _call(dev: torch.device, fn, *args):
         return fn(*args, torch._C._cuda_getCurrentRawStream(i))
 
 
-def _act(t, name):
-    """A contiguous 2-D activation of a supported type."""
-    if t is None:
-        raise MoeError(f"{name} is required")
-    if t.dtype not in _DTYPES or t.dim() != 2:
-        raise MoeError(f"{name}: a 2-D bf16, fp16 or fp32 tensor is expected, got {t.dtype} "
-                       f"{tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise MoeError(f"{name} must be contiguous")
-    return t
+def _native():
+    """The native part of the binding."""
+    return N._binding or N.load_binding(MoeError)
+
+
+def _status_for(t):
+    """Status words beside a tensor (None for what the call will refuse)."""
+    return new_status(t.device) if isinstance(t, torch.Tensor) and t.is_cuda else None
 
 
 def rng_state(seed: int, offset: int = 0, device="cuda") -> torch.Tensor:
@@ -290,47 +289,6 @@ def rng_state(seed: int, offset: int = 0, device="cuda") -> torch.Tensor:
     their masks. Change it (in place, under a captured graph) to draw new ones."""
     wrap = [(int(v) + 2 ** 63) % 2 ** 64 - 2 ** 63 for v in (seed, offset)]
     return torch.tensor(wrap, dtype=torch.int64, device=device)
-
-
-def _norm_setup(x, y, w_post, gate, w_next, eps, residual_scale, branch_scale, p, rng, first_row,
-                row_ids):
-    """The checks that residual_norm and its backward share; their configuration."""
-    shape, dt, dev = x.shape, x.dtype, x.device
-    T, H = shape
-    code = _DTYPES[dt]
-    if y is not None:
-        _need(y, "y", dt, shape, dev)
-    elif w_post is not None or gate is not None or p or w_next is None or residual_scale != 1.0:
-        raise MoeError("without y there is only the norm: w_next is required, and w_post, gate, "
-                       "p and residual_scale do not apply")
-    mode, small = N.MOE_GATE_NONE, None
-    if gate is not None:
-        g = gate.shape
-        if g == (H,):
-            mode, small = N.MOE_GATE_CHANNEL, gate
-        elif g == (T, 1):
-            mode, small = N.MOE_GATE_TOKEN, gate
-        elif g == shape:
-            mode = N.MOE_GATE_FULL
-            _need(gate, "gate", dt, shape, dev)
-        else:
-            raise MoeError(f"gate: shape {tuple(g)}, expected ({H},), ({T}, 1) or ({T}, {H})")
-    first = w_post if w_post is not None else w_next if w_next is not None else small
-    pd = torch.float32 if first is None else first.dtype
-    if pd is not torch.float32 and pd is not dt:
-        raise MoeError(f"parameters: dtype {pd}, expected torch.float32 or {dt}")
-    if w_post is not None:
-        _need(w_post, "w_post", pd, (H,), dev)
-    if w_next is not None:
-        _need(w_next, "w_next", pd, (H,), dev)
-    if small is not None:
-        _need(small, "gate", pd, small.shape, dev)
-    if p:
-        _need(rng, "rng", torch.int64, (2,), dev)
-    if row_ids is not None:
-        _need(row_ids, "row_ids", torch.int32, (T,), dev)
-    return N.MoeNormCfg(T, first_row, p, H, code, code if pd is dt else N.MOE_F32, mode, eps,
-                        residual_scale, branch_scale)
 
 
 def residual_norm(x, y=None, w_post=None, gate=None, w_next=None, eps: float = 1e-6,
@@ -345,27 +303,8 @@ def residual_norm(x, y=None, w_post=None, gate=None, w_next=None, eps: float = 1
     [T,H]) optional; weights fp32 or of x's type, a [T,H] gate of x's type. y=None: the norm
     before the first block. p, rng, first_row, row_ids: see dropout. r, n: outputs to write
     (r may be x, n may be y). Returns (r, n), n None without w_next; r is x without y."""
-    _act(x, "x")
-    dev = x.device
-    cfg = _norm_setup(x, y, w_post, gate, w_next, eps, residual_scale, branch_scale, p, rng,
-                      first_row, row_ids)
-    if y is None:
-        if r is not None:
-            raise MoeError("without y, r is x: no output to write")
-    elif r is None:
-        r = torch.empty_like(x)
-    else:
-        _need(r, "r", x.dtype, x.shape, dev)
-    if w_next is None:
-        if n is not None:
-            raise MoeError("n needs w_next")
-    elif n is None:
-        n = torch.empty_like(x)
-    else:
-        _need(n, "n", x.dtype, x.shape, dev)
-    _rc(_call(dev, N.load().moe_residual_norm, ctypes.byref(cfg), _p(x), _p(y), _p(w_post),
-              _p(gate), _p(w_next), _p(rng), _p(row_ids), _p(r), _p(n)), "moe_residual_norm")
-    return (x if y is None else r), n
+    return _native().residual_norm(x, y, w_post, gate, w_next, eps, residual_scale, branch_scale,
+                                   p, rng, first_row, row_ids, r, n)
 
 
 def residual_norm_backward(r, y=None, dr=None, dn=None, w_post=None, gate=None, w_next=None,
@@ -377,31 +316,9 @@ def residual_norm_backward(r, y=None, dr=None, dn=None, w_post=None, gate=None, 
     had no y), the other arguments are the forward's; dn is given exactly with w_next, dr may
     be None. dx, dy and a [T,H] gate's gradient have r's type, the others are fp32. The norm
     statistics and the dropout mask are recomputed; nothing else is kept from the forward."""
-    _act(r, "r")
-    dev, dt, shape = r.device, r.dtype, r.shape
-    cfg = _norm_setup(r, y, w_post, gate, w_next, eps, residual_scale, branch_scale, p, rng,
-                      first_row, row_ids)
-    _opt(dr, "dr", dt, shape, dev)
-    _opt(dn, "dn", dt, shape, dev)
-    if (dn is None) != (w_next is None):
-        raise MoeError("dn is given exactly with w_next")
-    if dr is None and dn is None:
-        raise MoeError("dr or dn is required")
-    lib, f32 = N.load(), torch.float32
-    dx = torch.empty_like(r)
-    dy = None if y is None else torch.empty_like(r)
-    dw_post = None if w_post is None else torch.empty_like(w_post, dtype=f32)
-    dgate = None if gate is None else torch.empty_like(
-        gate, dtype=dt if cfg.gate == N.MOE_GATE_FULL else f32)
-    dw_next = None if w_next is None else torch.empty_like(w_next, dtype=f32)
-    ref = ctypes.byref(cfg)
-    nbytes = lib.moe_residual_norm_workspace_bytes(ref)
-    ws = _ws(nbytes, dev, None)
-    _rc(_call(dev, lib.moe_residual_norm_backward, ref, _p(r), _p(y), _p(w_post), _p(gate),
-              _p(w_next), _p(rng), _p(row_ids), _p(dr), _p(dn), _p(dx), _p(dy), _p(dw_post),
-              _p(dgate), _p(dw_next), _p(ws), nbytes), "moe_residual_norm_backward")
-    g = {"dx": dx, "dy": dy, "dw_post": dw_post, "dgate": dgate, "dw_next": dw_next}
-    return {k: v for k, v in g.items() if v is not None}
+    return _native().residual_norm_backward(r, y, dr, dn, w_post, gate, w_next, eps,
+                                            residual_scale, branch_scale, p, rng, first_row,
+                                            row_ids)
 
 
 def dropout(x, p: float, rng, first_row: int = 0, row_ids=None, out=None):
@@ -409,14 +326,7 @@ def dropout(x, p: float, rng, first_row: int = 0, row_ids=None, out=None):
     out = x / P(keep) where kept, 0 elsewhere. The mask is a function of rng (rng_state()), the
     row and the column alone; row t is first_row + t, or row_ids[t], so a token keeps its mask
     in any batch. The gradient is dropout(dout) with the same p, rng and rows. out may be x."""
-    _act(x, "x")
-    dev, (T, H) = x.device, x.shape
-    _need(rng, "rng", torch.int64, (2,), dev)
-    _opt(row_ids, "row_ids", torch.int32, (T,), dev)
-    out = torch.empty_like(x) if out is None else _need(out, "out", x.dtype, x.shape, dev)
-    _rc(_call(dev, N.load().moe_dropout, T, H, _DTYPES[x.dtype], p, _p(x), _p(rng), first_row,
-              _p(row_ids), _p(out)), "moe_dropout")
-    return out
+    return _native().dropout(x, p, rng, first_row, row_ids, out)
 
 
 # ------------------------------------------------------------------ backward
@@ -599,23 +509,12 @@ def forward_host(cfg: Config, x_host, w_router, w13, w2, logit_bias=None, sel_bi
 
 # ------------------------------------------------------------------ experts in 4 bits
 
-def _mx_tiles(rows: int, K: int):
-    return -(-rows // 128), -(-K // 128), 512
-
-
 def mx_quantize(x, tiled: bool = True):
     """Rows of x [R,K] (bf16, fp16 or fp32, K a multiple of 32) in the microscaled 4-bit format
     (moe_mx_quantize): (codes [R,K/2], scales), both uint8. The scales are in the tensor core's
     tiles, [ceil(R/128), ceil(K/128), 512], as the products take them, or with tiled=False
     row-major, [R,K/32]."""
-    _act(x, "x")
-    dev, (R, K) = x.device, x.shape
-    codes = torch.empty(R, K // 2, dtype=torch.uint8, device=dev)
-    scales = torch.empty(-(-R // 128), -(-K // 128), 512, dtype=torch.uint8, device=dev) if tiled \
-        else torch.empty(R, K // 32, dtype=torch.uint8, device=dev)
-    _rc(_call(dev, N.load().moe_mx_quantize, R, K, _DTYPES[x.dtype], int(bool(tiled)), _p(x),
-              _p(codes), _p(scales)), "moe_mx_quantize")
-    return codes, scales
+    return _native().mx_quantize(x, tiled)
 
 
 def mx_weight(w):
@@ -640,18 +539,7 @@ def mx_weight(w):
 def mx_dequantize(codes, scales, dtype=torch.bfloat16):
     """The values of mx_quantize's codes [R,K/2] and scales (in tiles, or row-major [R,K/32]),
     rounded to dtype: [R,K]."""
-    dev = codes.device
-    if codes.dim() != 2 or dtype not in _DTYPES or codes.shape[1] % 16:
-        raise MoeError(f"codes {tuple(codes.shape)} to {dtype}: [R, K/2] with K a multiple of 32, "
-                       "and bf16, fp16 or fp32, are expected")
-    R, K = codes.shape[0], 2 * codes.shape[1]
-    _need(codes, "codes", torch.uint8, (R, K // 2), dev)
-    tiled = scales.dim() == 3
-    _need(scales, "scales", torch.uint8, _mx_tiles(R, K) if tiled else (R, K // 32), dev)
-    out = torch.empty(R, K, dtype=dtype, device=dev)
-    _rc(_call(dev, N.load().moe_mx_dequantize, R, K, _DTYPES[dtype], int(tiled), _p(codes),
-              _p(scales), _p(out)), "moe_mx_dequantize")
-    return out
+    return _native().mx_dequantize(codes, scales, dtype)
 
 
 def _mx_need(w, name, n, k, dev, lead=()):
@@ -667,26 +555,11 @@ def mx_grouped_gemm(codes, scales, offsets, w_codes, w_scales, swiglu: bool = Fa
     """Rows in 4 bits (mx_quantize, scales in tiles), grouped by offsets [E+1], times 4-bit weights
     (mx_weight of [E,N,K]): [R,N] bf16, or with swiglu silu(first N/2 columns) * last N/2, [R,N/2]
     (moe_mx_grouped_gemm). Rows outside every group are left as they were in out."""
-    dev = codes.device
-    if w_codes.dim() != 3 or codes.dim() != 2:
-        raise MoeError("codes [R, K/2] and w_codes [E, N, K/2] are expected")
-    R, K = codes.shape[0], 2 * codes.shape[1]
-    E, n = w_codes.shape[:2]
-    if n % (256 if swiglu else 128) or K % 128:
-        raise MoeError(f"N {n} and K {K}: multiples of {256 if swiglu else 128} and 128")
-    _need(codes, "codes", torch.uint8, (R, K // 2), dev)
-    _need(scales, "scales", torch.uint8, _mx_tiles(R, K), dev)
-    _need(offsets, "offsets", torch.int32, (E + 1,), dev)
-    _mx_need((w_codes, w_scales), "w", n, K, dev, (E,))
-    cols = n // 2 if swiglu else n
-    out = torch.empty(R, cols, dtype=torch.bfloat16, device=dev) if out is None else \
-        _need(out, "out", torch.bfloat16, (R, cols), dev)
-    st = new_status(dev) if status is None and check else status
-    _rc(_call(dev, N.load().moe_mx_grouped_gemm, R, K, n, E, int(bool(swiglu)), _p(codes),
-              _p(scales), _p(offsets), _p(w_codes), _p(w_scales), _p(out), _p(st)),
-        "moe_mx_grouped_gemm")
+    if check and status is None:
+        status = _status_for(codes)
+    out = _native().mx_grouped_gemm(codes, scales, offsets, w_codes, w_scales, swiglu, out, status)
     if check:
-        check_status(st)
+        check_status(status)
     return out
 
 
@@ -708,23 +581,12 @@ def mx_grouped_ffn(cfg: Config, x, dest_row, offsets, w13, w2, w13_s=None, w2_s=
     """The expert boundary with 4-bit experts (moe_mx_grouped_ffn): w13, w2 (and the shared
     expert's) as mx_weight() returned them, dest_row and offsets from permute(). Returns
     (y [T*K,H], y_shared [T,H] or None)."""
-    dev = x.device
-    T, H, E, K, Is = cfg.T, cfg.H, cfg.E, cfg.K, cfg.I_shared
-    _need(x, "x", torch.bfloat16, (T, H), dev)
-    _need(dest_row, "dest_row", torch.int32, (T, K), dev)
-    _need(offsets, "offsets", torch.int32, (E + 1,), dev)
-    w = _mx_experts(cfg, w13, w2, w13_s, w2_s, dev)
-    y = torch.empty(T * K, H, dtype=torch.bfloat16, device=dev)
-    y_s = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if Is else None
-    lib, ref = N.load(), ctypes.byref(cfg.c())
-    nbytes = lib.moe_workspace_bytes(ref, N.MOE_STAGE_MX_FFN)
-    ws = _ws(nbytes, dev, ws)
-    st = new_status(dev) if status is None and check else status
-    _rc(_call(dev, lib.moe_mx_grouped_ffn, ref, _p(x), _p(dest_row),
-              _p(offsets), *w, _p(y), _p(y_s), _p(st), _p(ws), nbytes), "moe_mx_grouped_ffn")
+    if check and status is None:
+        status = _status_for(x)
+    y = _native().mx_grouped_ffn(cfg, x, dest_row, offsets, w13, w2, w13_s, w2_s, ws, status)
     if check:
-        check_status(st)
-    return y, y_s
+        check_status(status)
+    return y
 
 
 def mx_forward(cfg: Config, x, w_router, w13, w2, logit_bias=None, sel_bias=None, token_mask=None,

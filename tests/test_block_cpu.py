@@ -158,7 +158,7 @@ def test_norm_pointer_combinations_rejected(lib):
         assert lib.moe_dropout(4, 64, 0, 0.5, x, rng, 0, None, out, None) == N.MOE_ERR_ARG
 
 
-def test_binding_refusals():
+def test_binding_refusals(lib):
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     w = torch.ones(64)
     bad = [lambda: moe.residual_norm(x.int(), x, w_next=w),
@@ -193,3 +193,10 @@ def test_rng_state_wraps():
     s = moe.rng_state(2 ** 64 - 1, 2 ** 63, device="cpu").tolist()
     assert s == [-1, -2 ** 63]
     assert moe.rng_state(5, 7, device="cpu").tolist() == [5, 7]
+
+
+def test_binding_fails_loudly_when_it_is_not_built(lib, monkeypatch, tmp_path):
+    monkeypatch.setattr(N, "BINDING_PATH", str(tmp_path / "missing.so"))
+    monkeypatch.setattr(N, "_binding", None)
+    with pytest.raises(RuntimeError, match="not built"):
+        moe.dropout(torch.zeros(2, 8), 0.5, moe.rng_state(1, device="cpu"))

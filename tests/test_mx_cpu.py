@@ -114,7 +114,7 @@ def test_layer_refusals(lib):
     assert lib.moe_mx_forward(ctypes.byref(c), *args, need, None) == N.MOE_ERR_ARG
 
 
-def test_binding_refusals():
+def test_binding_refusals(lib):
     x = torch.zeros(4, 128, dtype=torch.bfloat16)
     c, s = torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(1, 1, 512, dtype=torch.uint8)
     flat = torch.zeros(4, 4, dtype=torch.uint8)
