@@ -7,7 +7,8 @@
 // by the tensor core, fp32 accumulation in TMEM). The structure is the bf16 pair kernel's: a
 // cluster of two CTAs computes 256 rows by 256 columns, each CTA holding its 128 rows of A and
 // half of B's columns, so that a k-block (256 columns of K: 128 bytes a row) takes 32 KiB a CTA
-// for the 512 cycles its four instructions need.
+// for the 512 cycles its four instructions need. Where groups have few rows, single CTAs compute
+// tiles of 128 rows by the same 256 columns instead (launch_mx_gemm has the rule).
 //
 // Scales: an instruction reads them from TMEM, 4 bytes (4 blocks of 32) per row in a 32-bit
 // column for every 32 rows. Both operands keep them in tiles of 128 rows by 4 blocks (512 bytes,
@@ -34,7 +35,8 @@
 // PFLOP/s (the same kernel issuing its instructions on stale operands: 315 us, 7.0); the 30B-A3B
 // layer at 16384 tokens, 128 experts: gate_up 177 us (825 GFLOP; 133 us at that rate with the
 // rounding up to tiles), down 146 us (412 GFLOP, 537 MB of output: 82 us of writing); 24594 rows
-// over 256 experts of 2048 x 4096 (1.14 GB of weights, 174 us of reading) 222 us. What is left
+// over 256 experts of 2048 x 4096 (1.14 GB of weights, 174 us of reading) 222 us; 512 rows over 128
+// experts of 2048 x 768 (107 MB, 16 us) 21 us. What is left
 // is the gap between two tiles of a cluster, about 1000 cycles from the last instruction of one,
 // through its epilogue's first reads, to the first of the next (the price of the shared columns),
 // and for down the stores.
@@ -44,15 +46,12 @@
 namespace moe {
 namespace {
 
-constexpr int XM = 256;                 // rows per pair tile
 constexpr int XH = 128;                 // rows per CTA
-constexpr int XN = 256;                 // columns per pair tile (SwiGLU: 128 gate, 128 up)
+constexpr int XN = 256;                 // columns per tile (SwiGLU: 128 gate, 128 up)
 constexpr int XK = 256;                 // columns of K per stage
 constexpr uint32_t kXA = XH * XK / 2;   // 16 KiB
-constexpr uint32_t kXB = XH * XK / 2;   // 16 KiB: this CTA's half of the columns
 constexpr uint32_t kXSA = 1024;         // scales of 128 rows, two tiles of 4 blocks
 constexpr uint32_t kXSB = 2048;         // scales of 256 columns
-constexpr uint32_t kXStage = kXA + kXB + kXSA + kXSB;
 constexpr uint32_t kXBox = 32 * XK / 2; // a 32-row box of A
 constexpr int kXEpiWarps = 8;
 constexpr int kXThreads = 32 * (2 + kXEpiWarps);
@@ -63,13 +62,16 @@ constexpr uint16_t kXPair = 0x3;
 
 // Shared memory is split between operand stages and store tiles (32 rows x 64 columns of bf16 per
 // epilogue warp). Quantised outputs need no store tiles.
-template <int S, int BUFS>
+template <bool PAIR, int S, int BUFS>
 struct MxSmem {
+    static constexpr int kRows = PAIR ? 2 * XH : XH;                // rows per tile
+    static constexpr uint32_t kB = (PAIR ? 128u : 256u) * XK / 2;  // a CTA's columns of B
+    static constexpr uint32_t kStage = kXA + kB + kXSA + kXSB;
     static constexpr uint32_t kEpi = (uint32_t)BUFS * kXEpiWarps * 4096u;
     static constexpr int kBars = 2 * S + 6;
     static size_t bytes(int groups)
     {
-        return 1024 + (size_t)S * kXStage + kEpi + kBars * 8 + 16 +
+        return 1024 + (size_t)S * kStage + kEpi + kBars * 8 + 16 +
                (size_t)2 * (groups + 1) * sizeof(int32_t);
     }
 };
@@ -94,9 +96,9 @@ struct MxTile {
 };
 
 // rows of a group that starts at `beg`, tiled from the multiple of 128 below it
-__device__ __forceinline__ int mx_row_tiles(int beg, int end)
+__device__ __forceinline__ int mx_row_tiles(int beg, int end, int rows)
 {
-    return end > beg ? (end - (beg & ~127) + XM - 1) / XM : 0;
+    return end > beg ? (end - (beg & ~127) + rows - 1) / rows : 0;
 }
 
 // which of CTA `rank`'s four 32-row boxes hold rows of the group
@@ -111,7 +113,7 @@ __device__ __forceinline__ uint32_t mx_boxes(const MxTile& t, uint32_t rank)
     return m;
 }
 
-// kind::mxf4 with e2m1 operands (format 1), e8m0 scales (bit 23), M = 256, N = 256, both K-major;
+// kind::mxf4 with e2m1 operands (format 1), e8m0 scales (bit 23), both K-major;
 // the scale bytes of a 32-bit column that the instruction reads start at byte `id` (0 or 2)
 constexpr uint32_t mx_idesc(int m, int n, uint32_t id)
 {
@@ -119,23 +121,56 @@ constexpr uint32_t mx_idesc(int m, int n, uint32_t id)
            ((uint32_t)(m >> 4) << 24) | (id << 29);
 }
 
-__device__ __forceinline__ void mma_mxf4_pair(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc,
-                                              uint32_t sa, uint32_t sb, uint32_t accumulate)
+template <bool PAIR>
+__device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc,
+                                         uint32_t sa, uint32_t sb, uint32_t accumulate)
 {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
-        "[%5], p;\n\t}\n" ::"r"(d),
-        "l"(ad), "l"(bd), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
-        : "memory");
+    if (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+            "[%5], p;\n\t}\n" ::"r"(d),
+            "l"(ad), "l"(bd), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+            "[%5], p;\n\t}\n" ::"r"(d),
+            "l"(ad), "l"(bd), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+            : "memory");
 }
 
-// 512 bytes of both CTAs' shared memory (32 rows of 16) to 4 TMEM columns, in all lane quarters
-__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t desc)
+// 512 bytes of shared memory (32 rows of 16; of both CTAs of a pair) to 4 TMEM columns, a
+// multiple of 4, in all lane quarters
+template <bool PAIR>
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc)
 {
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-                 : "memory");
+    if (PAIR)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                     : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                     : "memory");
+}
+
+// arrive on `bar` (of both CTAs of a pair) once the tcgen05 work issued so far has completed
+template <bool PAIR>
+__device__ __forceinline__ void mx_commit(uint32_t bar)
+{
+    if (PAIR) mma_commit_pair_mc(bar, kXPair);
+    else mma_commit(bar);
+}
+
+// a TMA load whose bytes are counted on `bar`, the leader's of a pair
+template <bool PAIR>
+__device__ __forceinline__ void mx_load(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                        uint32_t bar)
+{
+    if (PAIR) tma_load_2d_pair(dst, map, x, y, bar);
+    else tma_load_2d(dst, map, x, y, bar);
 }
 
 // True in one lane of a converged warp. The loading and issuing roles run as whole warps whose
@@ -208,7 +243,9 @@ __device__ __forceinline__ float swiglu_fast(float g, float u)
     return g * r * u;
 }
 
-template <int MODE, int kXS, int BUFS>
+// PAIR: a cluster of two CTAs a tile of 256 rows; else one CTA a tile of 128, with all of B's
+// columns of the tile in its stages
+template <int MODE, bool PAIR, int kXS, int BUFS>
 __global__ void __launch_bounds__(kXThreads, 1)
     mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                    const __grid_constant__ CUtensorMap tmA32,
@@ -218,7 +255,9 @@ __global__ void __launch_bounds__(kXThreads, 1)
                    const __grid_constant__ CUtensorMap tmO, MxArgs args)
 {
     constexpr bool kGlu = MODE != MX_BF16;
-    using M = MxSmem<kXS, BUFS>;
+    using M = MxSmem<PAIR, kXS, BUFS>;
+    constexpr uint32_t kXB = M::kB, kXStage = M::kStage;
+    constexpr int XM = M::kRows, kCtas = PAIR ? 2 : 1;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_s = smem_u32(smem_raw);
     uint8_t* base = smem_raw + ((1024u - (raw_s & 1023u)) & 1023u);
@@ -242,9 +281,9 @@ __global__ void __launch_bounds__(kXThreads, 1)
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int G = args.groups;
-    const uint32_t rank = blockIdx.x & 1;  // clusters are pairs of consecutive blocks
+    const uint32_t rank = PAIR ? blockIdx.x & 1 : 0;  // clusters are pairs of consecutive blocks
     const bool leader = rank == 0;
-    const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+    const int cluster = blockIdx.x / kCtas, nclusters = gridDim.x / kCtas;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kXS; ++s) {
@@ -253,9 +292,9 @@ __global__ void __launch_bounds__(kXThreads, 1)
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(tfull_bar(a), 1);
-            mbar_init(tempty_bar(a), 2 * kXEpiWarps);  // a warp of either CTA each
+            mbar_init(tempty_bar(a), kCtas * kXEpiWarps);  // a warp each
         }
-        mbar_init(tover, kXEpiWarps);  // half of each CTA's epilogue warps
+        mbar_init(tover, kCtas * kXEpiWarps / 2);  // half of each CTA's epilogue warps
         mbar_init(drain, 1);
         misc[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -269,7 +308,10 @@ __global__ void __launch_bounds__(kXThreads, 1)
         prefetch_map(&tmSB);
         prefetch_map(&tmO);
     }
-    if (warp == 1) tmem_alloc_pair(smem_u32(misc), kXCols);
+    if (warp == 1) {
+        if (PAIR) tmem_alloc_pair(smem_u32(misc), kXCols);
+        else tmem_alloc(smem_u32(misc), kXCols);
+    }
     pdl_wait();
     // the groups' offsets, clamped, by all threads at once; then one warp counts row tiles
     for (int g = threadIdx.x; g <= G; g += kXThreads) {
@@ -289,7 +331,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         int sum = 0;
         for (int g = beg; g < end; ++g) {
             if (offs[g + 1] < offs[g]) bad = true;
-            sum += mx_row_tiles(offs[g], offs[g + 1]);
+            sum += mx_row_tiles(offs[g], offs[g + 1], XM);
         }
         int incl = sum;
 #pragma unroll
@@ -300,7 +342,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         int run = incl - sum;
         for (int g = beg; g < end; ++g) {
             prefix[g] = run;
-            run += mx_row_tiles(offs[g], offs[g + 1]);
+            run += mx_row_tiles(offs[g], offs[g + 1], XM);
         }
         if (lane == 31) prefix[G] = incl;
         if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0)
@@ -338,7 +380,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
         // -------------------------------------------------------------- TMA producer
         int stage = 0;
         uint32_t phase = 0, armed = 0, armed_phase = 0;
-        const uint32_t fb0 = (uint32_t)uniform((int)mapa_shared(full_bar(0), 0));
+        const uint32_t fb0 =
+            PAIR ? (uint32_t)uniform((int)mapa_shared(full_bar(0), 0)) : full_bar(0);
         const int kc = args.k / 128;  // scale tiles along K
         for (int t = cluster; t < total && !aborted(); t += nclusters) {
             const MxTile ti = decode(t);
@@ -362,19 +405,24 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 }
                 const uint32_t fb = fb0 + 8u * (uint32_t)stage, ss = (uint32_t)stage;
                 if (elect_one()) {
-                    if (leader) mbar_expect_tx(full_bar(stage), 2 * kXStage);
+                    if (leader) mbar_expect_tx(full_bar(stage), kCtas * kXStage);
                     if (mine == 15u) {
-                        tma_load_2d_pair(sA0 + ss * kXA, &tmA, kb * (XK / 2), arow, fb);
+                        mx_load<PAIR>(sA0 + ss * kXA, &tmA, kb * (XK / 2), arow, fb);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            tma_load_2d_pair(sA0 + ss * kXA + j * kXBox, &tmA32, kb * (XK / 2),
-                                             mine >> j & 1u ? arow + 32 * j : past, fb);
+                            mx_load<PAIR>(sA0 + ss * kXA + j * kXBox, &tmA32, kb * (XK / 2),
+                                          mine >> j & 1u ? arow + 32 * j : past, fb);
                     }
-                    tma_load_2d_pair(sB0 + ss * kXB, &tmB, kb * (XK / 2), brow, fb);
-                    tma_load_2d_pair(sSA0 + ss * kXSA, &tmSA, 0, sa + 2 * kb, fb);
-                    tma_load_2d_pair(sSB0 + ss * kXSB, &tmSB, 0, sb0 + 2 * kb, fb);
-                    tma_load_2d_pair(sSB0 + ss * kXSB + 1024u, &tmSB, 0, sb1 + 2 * kb, fb);
+                    if (PAIR) {
+                        mx_load<PAIR>(sB0 + ss * kXB, &tmB, kb * (XK / 2), brow, fb);
+                    } else {
+                        mx_load<PAIR>(sB0 + ss * kXB, &tmB, kb * (XK / 2), b0 * 128, fb);
+                        mx_load<PAIR>(sB0 + ss * kXB + kXB / 2, &tmB, kb * (XK / 2), b1 * 128, fb);
+                    }
+                    mx_load<PAIR>(sSA0 + ss * kXSA, &tmSA, 0, sa + 2 * kb, fb);
+                    mx_load<PAIR>(sSB0 + ss * kXSB, &tmSB, 0, sb0 + 2 * kb, fb);
+                    mx_load<PAIR>(sSB0 + ss * kXSB + 1024u, &tmSB, 0, sb1 + 2 * kb, fb);
                 }
                 __syncwarp();
                 armed |= 1u << stage;
@@ -417,10 +465,10 @@ __global__ void __launch_bounds__(kXThreads, 1)
                     const bool issuer = elect_one();
                     if (issuer) {
                         auto copy = [&](uint32_t c) {
-                            tmem_cp_scales_pair(tsa + 4u * c, sad + (uint64_t)(c * (512 >> 4)));
-                            tmem_cp_scales_pair(tsb + 8u * c, sbd + (uint64_t)(c * (512 >> 4)));
-                            tmem_cp_scales_pair(tsb + 8u * c + 4u,
-                                                sbd + (uint64_t)((1024 + c * 512) >> 4));
+                            tmem_cp_scales<PAIR>(tsa + 4u * c, sad + (uint64_t)(c * (512 >> 4)));
+                            tmem_cp_scales<PAIR>(tsb + 8u * c, sbd + (uint64_t)(c * (512 >> 4)));
+                            tmem_cp_scales<PAIR>(tsb + 8u * c + 4u,
+                                                 sbd + (uint64_t)((1024 + c * 512) >> 4));
                         };
                         copy(0);
                         if (both) copy(1);
@@ -435,15 +483,15 @@ __global__ void __launch_bounds__(kXThreads, 1)
                     }
                     if (issuer) {
                         auto mma = [&](uint32_t c, uint32_t accumulate) {
-                            mma_mxf4_pair(d, ad + 4u * c, bd + 4u * c, mx_idesc(XM, XN, 0),
-                                          tsa + 4u * c, tsb + 8u * c, accumulate);
-                            mma_mxf4_pair(d, ad + 4u * c + 2u, bd + 4u * c + 2u,
-                                          mx_idesc(XM, XN, 2), tsa + 4u * c, tsb + 8u * c, 1u);
+                            mma_mxf4<PAIR>(d, ad + 4u * c, bd + 4u * c, mx_idesc(XM, XN, 0),
+                                           tsa + 4u * c, tsb + 8u * c, accumulate);
+                            mma_mxf4<PAIR>(d, ad + 4u * c + 2u, bd + 4u * c + 2u,
+                                           mx_idesc(XM, XN, 2), tsa + 4u * c, tsb + 8u * c, 1u);
                         };
                         mma(0, kb != 0 ? 1u : 0u);
                         if (both) mma(1, 1u);
-                        mma_commit_pair_mc(empty_bar(stage), kXPair);
-                        if (kb == args.k_blocks - 1) mma_commit_pair_mc(tfull_bar(acc), kXPair);
+                        mx_commit<PAIR>(empty_bar(stage));
+                        if (kb == args.k_blocks - 1) mx_commit<PAIR>(tfull_bar(acc));
                     }
                     __syncwarp();
                     if (++stage == kXS) {
@@ -453,7 +501,10 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 }
                 if (!ok) break;
             }
-            if (elect_one()) mma_commit_pair(drain);
+            if (elect_one()) {
+                if (PAIR) mma_commit_pair(drain);
+                else mma_commit(drain);
+            }
             __syncwarp();
             wait_warp(drain, 0u, false);
         }
@@ -518,7 +569,9 @@ __global__ void __launch_bounds__(kXThreads, 1)
             const int64_t grow = ti.row0 + (int64_t)rank * XH + row;
             const bool valid = grow >= ti.row_beg && grow < ti.row_end;
             const int row_blk = (int)(ti.row0 + (int64_t)rank * XH + q * 32);
-            const bool full_blk = row_blk >= ti.row_beg && (int64_t)row_blk + 31 < ti.row_end;
+            // (without store tiles every row goes by itself)
+            const bool full_blk =
+                BUFS > 0 && row_blk >= ti.row_beg && (int64_t)row_blk + 31 < ti.row_end;
             if (kGlu) {
                 // this warp's 64 columns of h, 32 at a time
                 const int col = ti.n * (XN / 2) + 64 * half;
@@ -619,7 +672,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc_pair(tmem_base, kXCols);
+        if (PAIR) tmem_dealloc_pair(tmem_base, kXCols);
+        else tmem_dealloc(tmem_base, kXCols);
     }
 }
 
@@ -667,11 +721,25 @@ bool make_out_map(CUtensorMap* m, void* ptr, int64_t rows, int64_t n)
               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, int S, int BUFS>
+int column_tiles(const MxProblem& p)
+{
+    return p.swiglu ? p.n / (XN / 2) : (p.n + XN - 1) / XN;
+}
+
+// tiles at most: two partial row tiles per group that has rows, and the full ones
+int64_t most_tiles(const MxProblem& p, int rows)
+{
+    const int64_t partial = p.rows < p.groups ? p.rows : p.groups;
+    return (p.rows / rows + 2 * partial) * column_tiles(p);
+}
+
+template <int MODE, bool PAIR, int S, int BUFS>
 cudaError_t launch_mode(const MxProblem& p, cudaStream_t st)
 {
-    auto kernel = mx_gemm_kernel<MODE, S, BUFS>;
-    const size_t smem = MxSmem<S, BUFS>::bytes(p.groups);
+    auto kernel = mx_gemm_kernel<MODE, PAIR, S, BUFS>;
+    using M = MxSmem<PAIR, S, BUFS>;
+    constexpr int kCtas = PAIR ? 2 : 1;
+    const size_t smem = M::bytes(p.groups);
     if (smem > 232448) return cudaErrorInvalidValue;
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
@@ -696,14 +764,14 @@ cudaError_t launch_mode(const MxProblem& p, cudaStream_t st)
         return cudaErrorInvalidValue;
     ma = ma32;
     if (p.rows >= 66 && !make_codes_map(&ma, p.a, p.rows, p.k, XH)) return cudaErrorInvalidValue;
-    mo = ma32;  // quantised outputs are stored from registers
-    if (MODE != MX_SWIGLU_QUANT && p.rows >= 32 && !make_out_map(&mo, p.out, p.rows, p.n))
+    mo = ma32;  // without store tiles outputs are stored from registers
+    if (BUFS > 0 && p.rows >= 32 && !make_out_map(&mo, p.out, p.rows, p.n))
         return cudaErrorInvalidValue;
     MxArgs a{};
     a.k = p.k;
     a.k_blocks = (p.k + XK - 1) / XK;
     a.n = p.n;
-    a.n_tiles = glu ? p.n / (XN / 2) : (p.n + XN - 1) / XN;
+    a.n_tiles = column_tiles(p);
     a.groups = p.groups;
     a.rows = p.rows;
     a.offsets = p.offsets;
@@ -716,12 +784,12 @@ cudaError_t launch_mode(const MxProblem& p, cudaStream_t st)
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = kCtas;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(2 * 74, 1, 1);
+    cfg.gridDim = dim3(148, 1, 1);
     cfg.blockDim = dim3(kXThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -735,11 +803,9 @@ cudaError_t launch_mode(const MxProblem& p, cudaStream_t st)
         if (n <= 0) return cudaErrorInvalidConfiguration;
         max_clusters[dev] = n;
     }
-    // row tiles at most: two partial tiles per group that has rows, and the full ones
-    const int64_t partial = p.rows < p.groups ? p.rows : p.groups;
-    int64_t clusters = (p.rows / XM + 2 * partial) * a.n_tiles;
+    int64_t clusters = most_tiles(p, M::kRows);
     if (clusters > max_clusters[dev]) clusters = max_clusters[dev];
-    cfg.gridDim = dim3((unsigned)(2 * clusters), 1, 1);
+    cfg.gridDim = dim3((unsigned)(kCtas * clusters), 1, 1);
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, ma, ma32, mb, msa, ms, mo, a);
 }
@@ -749,11 +815,22 @@ cudaError_t launch_mode(const MxProblem& p, cudaStream_t st)
 cudaError_t launch_mx_gemm(const MxProblem& p, cudaStream_t st)
 {
     if (p.k % 128 != 0 || p.n % 128 != 0) return cudaErrorInvalidValue;
+    // At few rows a group most of a pair's 256 rows are padding, and one CTA a tile has twice as
+    // many tiles in flight, each done in half the instructions. Measured, pairs against single
+    // CTAs, in us: 512 rows over 128 experts, 2048 x 768, 27.3 against 21.0; 64 over 64, 1536 x
+    // 2048 with SwiGLU, 22.7 / 16.7; 8192 over 256, 2048 x 4096 with SwiGLU, 221 / 198; at 64 rows
+    // a group 37.0 / 37.3 and 51.3 / 48.8; at 128 42.7 / 51.4 and 59.1 / 61.9. Both give the same
+    // bits: the row tile of an instruction is no part of a row's arithmetic.
+    if (p.rows <= 64 * (int64_t)p.groups) {
+        if (!p.swiglu) return launch_mode<MX_BF16, false, 4, 0>(p, st);
+        return p.out_codes != nullptr ? launch_mode<MX_SWIGLU_QUANT, false, 4, 0>(p, st)
+                                      : launch_mode<MX_SWIGLU, false, 4, 0>(p, st);
+    }
     // (four stages and two store tiles a warp instead of five and one measured within 2 % either
     // way for plain products of K = 256 .. 4096)
-    if (!p.swiglu) return launch_mode<MX_BF16, 5, 1>(p, st);
-    return p.out_codes != nullptr ? launch_mode<MX_SWIGLU_QUANT, 6, 0>(p, st)
-                                  : launch_mode<MX_SWIGLU, 5, 1>(p, st);
+    if (!p.swiglu) return launch_mode<MX_BF16, true, 5, 1>(p, st);
+    return p.out_codes != nullptr ? launch_mode<MX_SWIGLU_QUANT, true, 6, 0>(p, st)
+                                  : launch_mode<MX_SWIGLU, true, 5, 1>(p, st);
 }
 
 }  // namespace moe

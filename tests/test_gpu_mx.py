@@ -188,6 +188,25 @@ def test_a_row_keeps_its_bits_anywhere():
         assert eq(run(list(range(600)), [0, 100, 500, 600], glu), full)
 
 
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("sizes", [[64] * 4, [65, 64, 64, 64], [3, 250, 0, 3], [0, 300, 1, 1],
+                                   [1] * 150, [130, 5] * 30])
+def test_few_and_many_rows_a_group(sizes, glu):
+    """Up to 64 rows a group on average, and above, where the row tiles change."""
+    x, w, off = make_product(sizes, 384 + 128 * glu, 384, seed=len(sizes),
+                             extra=64 * (sizes[0] == 0))
+    out = moe.mx_grouped_gemm(*moe.mx_quantize(x),
+                              torch.tensor(off, dtype=torch.int32, device=DEV),
+                              *moe.mx_weight(w), swiglu=glu)
+    check_product(out[:off[-1]], x[:off[-1]], w, off, glu, 384)
+    lone = sum(sizes[:2]) - 1  # the second group's last row, computed by itself
+    one = moe.mx_grouped_gemm(*moe.mx_quantize(x[lone:lone + 1]),
+                              torch.tensor([0, 0, 1] + [1] * (len(sizes) - 2),
+                                           dtype=torch.int32, device=DEV),
+                              *moe.mx_weight(w), swiglu=glu)
+    assert eq(one, out[lone:lone + 1])
+
+
 def test_nan_blocks_reach_their_results_alone():
     x, w, off = make_product([200, 100], 256, 512, seed=3)
     offs = torch.tensor(off, dtype=torch.int32, device=DEV)
@@ -323,6 +342,17 @@ def test_tokens_keep_their_bits_in_any_batch():
     kw = dict(logit_bias=d["logit_bias"])
     full = moe.mx_forward(cfg, d["x"], d["w_router"], **q, **kw)
     for sel in (slice(0, 1), slice(37, 165), torch.randperm(400, device=DEV)):
+        x = d["x"][sel].contiguous()
+        part = moe.mx_forward(cfg.with_T(x.shape[0]), x, d["w_router"], **q, **kw)
+        assert eq(part, full[sel])
+
+
+def test_tokens_keep_their_bits_across_the_row_tiles():
+    """1100 tokens have 68 rows an expert on average, 500 and 1 have fewer than 64."""
+    cfg, d, q, _ = layer("qwen3_30b_a3b", 1100)
+    kw = dict(logit_bias=d["logit_bias"])
+    full = moe.mx_forward(cfg, d["x"], d["w_router"], **q, **kw)
+    for sel in (slice(3, 4), slice(600, 1100)):
         x = d["x"][sel].contiguous()
         part = moe.mx_forward(cfg.with_T(x.shape[0]), x, d["w_router"], **q, **kw)
         assert eq(part, full[sel])
