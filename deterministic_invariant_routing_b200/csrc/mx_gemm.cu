@@ -72,7 +72,7 @@ struct MxSmem {
     static size_t bytes(int groups)
     {
         return 1024 + (size_t)S * kStage + kEpi + kBars * 8 + 16 +
-               (size_t)2 * (groups + 1) * sizeof(int32_t);
+               ((size_t)2 * (groups + 1) + kXThreads / 32) * sizeof(int32_t);
     }
 };
 
@@ -278,6 +278,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
     int32_t* prefix = reinterpret_cast<int32_t*>(misc + 4);  // [groups + 1] row tiles before g
     int32_t* offs = prefix + (args.groups + 1);              // [groups + 1]
+    int32_t* totals = offs + (args.groups + 1);              // [warps] row tiles of a warp's groups
 
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int G = args.groups;
@@ -312,47 +313,55 @@ __global__ void __launch_bounds__(kXThreads, 1)
         if (PAIR) tmem_alloc_pair(smem_u32(misc), kXCols);
         else tmem_alloc(smem_u32(misc), kXCols);
     }
+    // (the barriers above are ready for the other CTA: fenced, and waited for below)
+    if (PAIR) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
     pdl_wait();
-    // the groups' offsets, clamped, by all threads at once; then one warp counts row tiles
-    for (int g = threadIdx.x; g <= G; g += kXThreads) {
-        int o = args.offsets != nullptr ? args.offsets[g] : (g == 0 ? 0 : (int)args.rows);
-        if (o < 0 || o > args.rows) {
-            if (blockIdx.x == 0) status_add(args.status, MOE_ST_BAD_ROWS, 1);
-            o = o < 0 ? 0 : (int)args.rows;
+    // The groups' offsets, clamped, and the row tiles before each group: a group a thread, scanned
+    // within a warp and then over the warps' totals. (Offsets by all threads and then four groups
+    // a lane of one warp took 1600 cycles at 128 groups, of the 20 000 of a decode product.)
+    int carry = 0;
+    for (int g0 = 0; g0 < G; g0 += kXThreads) {
+        const int g = g0 + (int)threadIdx.x;
+        int n = 0;
+        if (g < G) {
+            const int rows = (int)args.rows;
+            const int raw0 = args.offsets != nullptr ? args.offsets[g] : 0;
+            const int raw1 = args.offsets != nullptr ? args.offsets[g + 1] : rows;
+            const int beg = min(max(raw0, 0), rows), end = min(max(raw1, 0), rows);
+            n = mx_row_tiles(beg, end, XM);
+            offs[g] = beg;
+            if (g == G - 1) offs[G] = end;
+            if (blockIdx.x == 0) {
+                const int bad = (end < beg) + (raw1 != end) + (g == 0 && raw0 != beg);
+                if (bad) status_add(args.status, MOE_ST_BAD_ROWS, bad);
+            }
         }
-        offs[g] = o;
-    }
-    __syncthreads();
-    if (warp == 2) {
-        bool bad = false;
-        const int per = (G + 31) / 32;
-        const int beg = lane * per < G ? lane * per : G;
-        const int end = beg + per < G ? beg + per : G;
-        int sum = 0;
-        for (int g = beg; g < end; ++g) {
-            if (offs[g + 1] < offs[g]) bad = true;
-            sum += mx_row_tiles(offs[g], offs[g + 1], XM);
-        }
-        int incl = sum;
+        int incl = n;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int o = __shfl_up_sync(0xffffffffu, incl, off);
             if (lane >= off) incl += o;
         }
-        int run = incl - sum;
-        for (int g = beg; g < end; ++g) {
-            prefix[g] = run;
-            run += mx_row_tiles(offs[g], offs[g + 1], XM);
+        if (g0 != 0) __syncthreads();  // the totals of the 320 groups before are read
+        if (lane == 31) totals[warp] = incl;
+        __syncthreads();
+        int before = 0, all = 0;
+#pragma unroll
+        for (int w = 0; w < kXThreads / 32; ++w) {
+            const int v = totals[w];
+            before += w < warp ? v : 0;
+            all += v;
         }
-        if (lane == 31) prefix[G] = incl;
-        if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0)
-            status_add(args.status, MOE_ST_BAD_ROWS, 1);
+        if (g < G) prefix[g] = carry + before + incl - n;
+        carry += all;
     }
+    if (threadIdx.x == 0) prefix[G] = carry;
     tc_fence_before();
-    cluster_sync();
+    __syncthreads();
+    if (PAIR) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     tc_fence_after();
     const uint32_t tmem_base = (uint32_t)uniform((int)misc[0]);
-    const int total = uniform(prefix[G] * args.n_tiles);
+    const int total = uniform(carry * args.n_tiles);
     // a bounded wait of a whole warp: true when every lane's completed
     auto wait_warp = [&](uint32_t bar, uint32_t parity, bool honour_abort = true) -> bool {
         return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, args.status,
@@ -363,11 +372,16 @@ __global__ void __launch_bounds__(kXThreads, 1)
         MxTile ti;
         const int mt = t / args.n_tiles;
         ti.n = t - mt * args.n_tiles;
-        int lo = 0, hi = G - 1;
-        while (lo < hi) {  // the last group with prefix[g] <= mt: empty groups have no tile
-            const int mid = (lo + hi + 1) >> 1;
-            if (prefix[mid] <= mt) lo = mid;
-            else hi = mid - 1;
+        // the last group with prefix[g] <= mt (empty groups have no tile), the warp's 32 lanes
+        // looking at as many places of [lo, lo + span) at a time
+        int lo = 0;
+        for (int span = G; span > 1;) {
+            const int step = (span + 31) / 32;
+            const int g = lo + lane * step;
+            const uint32_t m = __ballot_sync(0xffffffffu, lane * step < span && prefix[g] <= mt);
+            const int last = 31 - __clz(m);  // lane 0's place always qualifies
+            span = min(step, span - last * step);
+            lo += last * step;
         }
         ti.g = lo;
         ti.row_beg = offs[lo];
@@ -513,9 +527,13 @@ __global__ void __launch_bounds__(kXThreads, 1)
         const int q = warp & 3;  // TMEM lanes 32 q .. 32 q + 31
         const int row = q * 32 + lane;
         const int half = (warp - 2) >> 2;  // two warps a lane quarter: the first and last chunks
-        const uint32_t tempty_leader0 = mapa_shared(tempty_bar(0), 0);
-        const uint32_t tempty_leader1 = mapa_shared(tempty_bar(1), 0);
-        const uint32_t tover_leader = mapa_shared(tover, 0);
+        const uint32_t tempty_leader0 = PAIR ? mapa_shared(tempty_bar(0), 0) : tempty_bar(0);
+        const uint32_t tempty_leader1 = PAIR ? mapa_shared(tempty_bar(1), 0) : tempty_bar(1);
+        const uint32_t tover_leader = PAIR ? mapa_shared(tover, 0) : tover;
+        auto arrive = [](uint32_t bar) {
+            if (PAIR) mbar_arrive_cluster(bar);
+            else mbar_arrive(bar);
+        };
         // Output: 32 rows x 64 columns of bf16 (128 bytes a row, 128-byte swizzle) through shared
         // memory and one TMA store where all 32 rows belong to the group, else row by row.
         const uint32_t ebuf0 = sE0 + (uint32_t)(warp - 2) * (BUFS * 4096u);
@@ -564,7 +582,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
             auto release_shared = [&]() {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(tover_leader);
+                if (lane == 0) arrive(tover_leader);
             };
             const int64_t grow = ti.row0 + (int64_t)rank * XH + row;
             const bool valid = grow >= ti.row_beg && grow < ti.row_end;
@@ -572,7 +590,10 @@ __global__ void __launch_bounds__(kXThreads, 1)
             // (without store tiles every row goes by itself)
             const bool full_blk =
                 BUFS > 0 && row_blk >= ti.row_beg && (int64_t)row_blk + 31 < ti.row_end;
-            if (kGlu) {
+            if (!__any_sync(0xffffffffu, valid)) {
+                // no row of the group: decode-sized groups leave the exponentials of one quarter
+                if (over) release_shared();
+            } else if (kGlu) {
                 // this warp's 64 columns of h, 32 at a time
                 const int col = ti.n * (XN / 2) + 64 * half;
                 uint32_t codes[8], scales = 0;
@@ -662,13 +683,14 @@ __global__ void __launch_bounds__(kXThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(acc ? tempty_leader1 : tempty_leader0);
+            if (lane == 0) arrive(acc ? tempty_leader1 : tempty_leader0);
         }
         if (lane == 0) bulk_wait_all();
     }
 
     tc_fence_before();
-    cluster_sync();
+    if (PAIR) cluster_sync();  // (with a release and an acquire: about 900 cycles)
+    else __syncthreads();
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
