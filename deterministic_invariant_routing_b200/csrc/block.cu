@@ -15,8 +15,8 @@
 // in fact is instructions: at 16-bit types a row pass leaves about 20 of them an element, and
 // the mask alone takes 8. Hence the packed fp32 arithmetic (F2), the kernels without branches for
 // the usual call, and the shuffles that add two values at once. Measured on B200:
-//   forward, 16384 x 2048 bf16, channel gate, dropout: 56 us (268 MB; 41 us at the copy's rate)
-//   backward, 8192 x 4096 bf16, the same:              96 us (403 MB; 61 us)
+//   forward, 16384 x 2048 bf16, channel gate, dropout: 45 us (268 MB; 41 us at the copy's rate)
+//   backward, 8192 x 4096 bf16, the same:              97 us (403 MB; 61 us)
 //
 // Parameter gradients are column sums over tokens: block b of a grid whose size is a function
 // of (T, H, type) adds rows b, b + blocks, ... into its registers and writes one partial row; a
@@ -141,10 +141,12 @@ __device__ __forceinline__ void drop2(const uint32_t (&w)[4], uint32_t threshold
 }
 
 // What a call has: kAny looks as it goes; kAll and kAllDrop are the usual call, with both norms
-// (backward: dr and room for the ring too), fp32 parameters and rows that fill their threads,
-// without and with dropout. Bound by instructions, the looking costs: a fifth of the backward's
+// (backward: dr and room for the ring too), fp32 parameters and rows that fill their threads
+// (FULL in the kernel over many rows), without and with dropout. Bound by instructions, the looking costs: a fifth of the backward's
 // were branches and their constants.
 enum { kAny = 0, kAll = 1, kAllDrop = 2 };
+
+constexpr int kRowsAhead = 2;  // rows on their way in residual_norm_rows_kernel
 
 // one row per block of blockDim.x <= MAXT threads, or (MAXT = 32) one per warp, threadIdx.y the row
 template <int DT, int V, int MAXT, int MODE>
@@ -260,6 +262,190 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT)
             for (int e = 0; e < 4; ++e) q[e] = mul2(mul2(q[e], inv), w[e]);
             set2(x[i], q);
             x[i].store(a.n, row + v);
+        }
+    }
+}
+
+// The same over many rows: a block takes one row after the other, with the weights in registers
+// and the next rows on their way to shared memory (cp.async; a warp copies its own vectors, so
+// no barrier). The arithmetic is the kernel's above, value for value; a place past the row's end
+// holds zeros, which add nothing, and only its stores are left out. 16 warps an SM with 128
+// registers each and no look at the weights again: 16384 x 2048 bf16 44.8 us, against 55 for the
+// kernel above at 32 warps (8192 x 4096: 46.8 against 59).
+// (FULL: rows fill their threads; without these looks 45 us instead of 46.5.)
+template <int DT, int MAXT, int MODE, bool FULL>
+__global__ void __launch_bounds__(MAXT, 512 / MAXT)
+    residual_norm_rows_kernel(const __grid_constant__ NormArgs a)
+{
+    constexpr int V = 2, W16 = DT == MOE_F32 ? 2 : 1;  // vectors a thread, their 16-byte words
+    constexpr bool ALL = MODE != kAny;
+    const bool post = ALL || a.w_post != nullptr, next = ALL || a.w_next != nullptr;
+    const bool branch = ALL || a.y != nullptr, param_f32 = ALL || a.param_f32;
+    const bool drop = MODE == kAllDrop || (MODE == kAny && a.threshold != 0);
+    extern __shared__ uint4 ring[];
+    __shared__ __align__(16) float red[2 * kRed];
+    int half = 0;
+    red_init(red, 2 * kRed);
+    pdl_wait();
+    const int tid = threadIdx.x, step = blockDim.x, nvec = a.nvec, gate_mode = a.gate_mode;
+    const bool last_in = FULL || tid + step < nvec;  // the first vector always is
+    F2 wp[V][4], wn[V][4], wg[V][4];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) wp[i][e] = wn[i][e] = wg[i][e] = f2(0.0f);
+        if (i == 0 || last_in) {
+            const int v = tid + i * step;
+            if (post) load_param2<DT>(a.w_post, param_f32, v, wp[i]);
+            if (next) load_param2<DT>(a.w_next, param_f32, v, wn[i]);
+            if (gate_mode == MOE_GATE_CHANNEL) load_param2<DT>(a.gate, param_f32, v, wg[i]);
+        }
+    }
+    Philox ph;
+    if (drop) ph = philox_load(a.rng);
+    // A stage: x and y, V vectors a thread each. A warp's 32 vectors are W16 x 32 words in a row;
+    // lane l copies words l (and 32 + l), so that a copy's bytes are consecutive, and reads words
+    // W16 l and up, its own vector.
+    const int lane = tid & 31, first = tid - lane;
+    const uint32_t array16 = (uint32_t)(W16 * step) * 16u, stage_bytes = 2 * V * array16;
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring) + (uint32_t)first * (W16 * 16u);
+    const uint32_t end = base + kRowsAhead * stage_bytes;
+    if (!FULL) {  // the places past a row's end stay zero
+        for (int k = tid; k < (int)(kRowsAhead * stage_bytes / 16u); k += step)
+            ring[k] = make_uint4(0u, 0u, 0u, 0u);
+        __syncthreads();
+    }
+    auto fetch = [&](uint32_t at, int64_t t) {
+        if (t < a.T) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+#pragma unroll
+                    for (int h = 0; h < W16; ++h) {
+                        const int word = (first + i * step) * W16 + 32 * h + lane;
+                        if ((FULL || word < nvec * W16) && (k == 0 || branch))
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                             at + (uint32_t)(k * V + i) * array16 +
+                                             (uint32_t)(32 * h + lane) * 16u),
+                                         "l"(static_cast<const uint4*>(k ? a.y : a.x) +
+                                             t * nvec * W16 + word)
+                                         : "memory");
+                    }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    uint32_t at = base;
+    auto get = [&](int k, int i, F2 (&f)[4]) {
+        uint4 w[W16];
+#pragma unroll
+        for (int h = 0; h < W16; ++h)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[h].x), "=r"(w[h].y), "=r"(w[h].z), "=r"(w[h].w)
+                         : "r"(at + (uint32_t)(k * V + i) * array16 +
+                               (uint32_t)(W16 * lane + h) * 16u)
+                         : "memory");
+        Vec8<DT> q;
+        q.load(w, 0);
+        get2(q, f);
+    };
+    for (int s = 0; s < kRowsAhead; ++s)
+        fetch(base + (uint32_t)s * stage_bytes, blockIdx.x + (int64_t)s * gridDim.x);
+    const F2 rs = f2(a.residual_scale);
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRowsAhead - 1) : "memory");
+        if (W16 > 1) __syncwarp();
+        const int64_t row = t * nvec;
+        Vec8<DT> o[V];
+        F2 acc = f2(0.0f);
+        float ss[1];
+        if (branch) {
+            F2 z[V][4];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                get(1, i, z[i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc = fma2(z[i][e], z[i][e], acc);
+            }
+            uint32_t mask[V][4];
+            if (drop) {
+                const uint32_t rid = row_id(a, t);
+                uint32_t col[V], rows[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    col[i] = (uint32_t)(tid + i * step);
+                    rows[i] = rid;
+                }
+                philox8n<V>(ph, col, rows, mask);
+            }
+            float scale = a.branch_scale * (drop ? a.inv_keep : 1.0f);
+            if (post) {
+                ss[0] = sum2(acc);
+                row_sum<1, MAXT>(ss, red, half);
+                scale *= inv_rms(ss[0], a);
+            }
+            if (gate_mode == MOE_GATE_TOKEN) scale *= load_param<DT>(a.gate, param_f32, t);
+            const F2 sc = f2(scale);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                F2 q[4];
+                const int64_t v = row + tid + i * step;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[i][e] = mul2(z[i][e], sc);
+                if (post) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[i][e] = mul2(z[i][e], wp[i][e]);
+                }
+                if (drop) drop2(mask[i], a.threshold, z[i]);
+                if (gate_mode == MOE_GATE_CHANNEL) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[i][e] = mul2(z[i][e], wg[i][e]);
+                } else if (gate_mode == MOE_GATE_FULL && (i == 0 || last_in)) {
+                    o[i].load(a.gate, v);
+                    get2(o[i], q);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[i][e] = mul2(z[i][e], q[e]);
+                }
+                get(0, i, q);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) q[e] = fma2(rs, q[e], z[i][e]);
+                set2(o[i], q);
+                if (i == 0 || last_in) o[i].store(a.r, v);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                F2 q[4];
+                get(0, i, q);
+                set2(o[i], q);
+            }
+        }
+        acc = f2(0.0f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            F2 q[4];
+            get2(o[i], q);  // the rounded r (past the row's end 0 times a NaN scale may be NaN)
+            if (i == 0 || last_in) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc = fma2(q[e], q[e], acc);
+            }
+        }
+        if (W16 > 1) __syncwarp();  // the warp has read the stage
+        fetch(at, t + (int64_t)kRowsAhead * gridDim.x);
+        at += stage_bytes;
+        if (at == end) at = base;
+        if (!next) continue;
+        ss[0] = sum2(acc);
+        row_sum<1, MAXT>(ss, red, half);
+        const F2 inv = f2(inv_rms(ss[0], a));
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            F2 q[4];
+            get2(o[i], q);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) q[e] = mul2(mul2(q[e], inv), wn[i][e]);
+            set2(o[i], q);
+            if (i == 0 || last_in) o[i].store(a.n, row + tid + i * step);
         }
     }
 }
@@ -754,6 +940,34 @@ cudaError_t norm_fwd_variant(const NormArgs& a, dim3 grid, dim3 block, cudaStrea
     return launch_pdl(kernel, grid, block, 0, st, a);
 }
 
+template <int DT, int MAXT>
+cudaError_t norm_rows(const NormArgs& a, unsigned blocks, dim3 block, cudaStream_t st)
+{
+    const bool all = a.y != nullptr && a.w_post != nullptr && a.w_next != nullptr && a.param_f32;
+    const bool drop = a.threshold != 0, full = a.nvec == 2 * (int)block.x;
+    const int which = !all ? 0 : 1 + 2 * full + drop;
+    auto kernel = !all   ? residual_norm_rows_kernel<DT, MAXT, kAny, false>
+                  : full ? (drop ? residual_norm_rows_kernel<DT, MAXT, kAllDrop, true>
+                                 : residual_norm_rows_kernel<DT, MAXT, kAll, true>)
+                         : (drop ? residual_norm_rows_kernel<DT, MAXT, kAllDrop, false>
+                                 : residual_norm_rows_kernel<DT, MAXT, kAll, false>);
+    const size_t smem = (size_t)kRowsAhead * 4 * (DT == MOE_F32 ? 32 : 16) * block.x;
+    if (smem > 48000) {  // fp32 above 187 threads, others above 375
+        int dev = 0;
+        cudaError_t err = cudaGetDevice(&dev);
+        if (err != cudaSuccess) return err;
+        if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+        static bool attr_set[5][64] = {};
+        if (!attr_set[which][dev]) {
+            err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kRowsAhead * 4 * 32 * MAXT);
+            if (err != cudaSuccess) return err;
+            attr_set[which][dev] = true;
+        }
+    }
+    return launch_pdl(kernel, dim3(blocks), block, smem, st, a);
+}
+
 template <int DT>
 cudaError_t norm_fwd(const NormArgs& a, cudaStream_t st)
 {
@@ -764,6 +978,13 @@ cudaError_t norm_fwd(const NormArgs& a, cudaStream_t st)
                         : norm_fwd_variant<DT, 2, 32>(a, grid, block, st);
     }
     const dim3 grid((unsigned)a.T), block(s.threads);
+    // With two rows or more for every block that fits, rows one after the other: of 2048 bf16, 600
+    // rows (592 blocks) take 3.9 us by blocks of their own and 4.1 so, 1200 6.5 and 5.7, 4800 17.6
+    // and 15.7, 16384 55 and 45.
+    const int64_t blocks = 148 * (512 / s.threads);  // 0 above 512 threads
+    if (blocks > 0 && a.T >= 2 * blocks)
+        return s.threads <= 256 ? norm_rows<DT, 256>(a, (unsigned)blocks, block, st)
+                                : norm_rows<DT, 512>(a, (unsigned)blocks, block, st);
     if (s.threads <= 256) return norm_fwd_variant<DT, 2, 256>(a, grid, block, st);
     if (s.threads <= 512) return norm_fwd_variant<DT, 2, 512>(a, grid, block, st);
     return norm_fwd_variant<DT, 2, 1024>(a, grid, block, st);

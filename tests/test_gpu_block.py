@@ -5,8 +5,8 @@ is rounded once, off by at most eps(t) / 2 of its value; before that every value
 expression. A sum over a row has a depth of at most 16 (a thread's elements) + 5 (shuffle) + 32
 (warps) roundings, the rest of the chain fewer than 11: 64 roundings of 2^-24 relative to the
 sum of the terms' magnitudes bound both (the norms divide by a root of such a sum, which halves
-it). A parameter gradient adds rows of a group (at most ceil(T / groups)), groups / 8 partials
-and 8 slices to that; T <= 4200 here keeps the depth below 64 + 80 + 74 + 8 < 256.
+it). A parameter gradient adds rows of a group (at most ceil(T / groups)), groups / 16 partials
+and 16 slices to that; T <= 4200 here keeps the depth below 64 + 80 + 74 + 16 < 256.
 n is compared with the norm of the r that the GPU returned, its definition."""
 import numpy as np
 import pytest
@@ -152,6 +152,49 @@ def test_rows_do_not_depend_on_the_batch(H):
         assert raw(rs) == raw(r[sel]) and raw(ns) == raw(n[sel])
         for k in ("dx", "dy", "dgate"):
             assert raw(gs[k]) == raw(g[k][sel]), k
+
+
+MANY = [(520, *MODES[1]), (1000, *MODES[3]), (2048, *MODES[1]), (2048, "channel", True, True, 0.0),
+        (2048, "none", True, True, 0.3), (4000, *MODES[2]), (4096, *MODES[4]), (4104, *MODES[1]),
+        (5120, *MODES[3]), (1032, *MODES[5]), (2048, *MODES[6]), (8192, *MODES[1])]
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_many_rows(dt, case):
+    """Calls whose rows outnumber the blocks that are resident at once (at most 512 threads an
+    SM, two vectors of 8 a thread): every row is right and has the bits it has in a call of few
+    rows, with non-finite rows among them, and in place."""
+    H, gate, post, nxt, p = MANY[case]
+    dtype, threads = TYPES[dt], -(-H // 512) * 32
+    T = 2 * 148 * (512 // threads) + 3
+    v = make(T, H, dtype, gate, post, nxt, seed=case, params=dtype if case % 3 == 2 else
+             torch.float32)
+    rng = moe.rng_state(5, case, device=DEV)
+    kw = dict(w_post=v["w_post"], w_next=v["w_next"], residual_scale=0.5, p=p, rng=rng)
+    r, n = moe.residual_norm(v["x"], v["y"], gate=v["gate"], **kw)
+    mask = mask_of(T, H, p, 5, case)
+    ref, mag = R.forward64(d64(v["x"]), d64(v["y"]), d64(v["w_post"]), d64(v["gate"]), mask,
+                           EPS, 0.5, 1.0)
+    check(r, ref, mag, dtype, "r")
+    if nxt:
+        ref = R.norm64(r.double(), d64(v["w_next"]), EPS)
+        check(n, ref, ref.abs(), dtype, "n")
+        check(moe.residual_norm(v["x"], w_next=v["w_next"])[1],
+              R.norm64(d64(v["x"]), d64(v["w_next"]), EPS),
+              R.norm64(d64(v["x"]), d64(v["w_next"]), EPS).abs(), dtype, "norm alone")
+    v["y"][7, 100], v["y"][T - 2, 3], v["x"][9, H - 1] = float("nan"), float("inf"), float("inf")
+    r, n = moe.residual_norm(v["x"], v["y"], gate=v["gate"], **kw)
+    for a, b in ((0, 1), (5, 105), (T - 40, T)):
+        g = v["gate"] if v["gate"] is None or gate == "channel" else v["gate"][a:b].contiguous()
+        r1, n1 = moe.residual_norm(v["x"][a:b], v["y"][a:b], gate=g, first_row=a, **kw)
+        assert raw(r1) == raw(r[a:b]) and (not nxt or raw(n1) == raw(n[a:b]))
+        if nxt:
+            whole = moe.residual_norm(v["x"], w_next=v["w_next"])[1]
+            assert raw(whole[a:b]) == raw(moe.residual_norm(v["x"][a:b], w_next=v["w_next"])[1])
+    x, y = v["x"].clone(), v["y"].clone()
+    moe.residual_norm(x, y, gate=v["gate"], r=x, n=y if nxt else None, **kw)
+    assert raw(x) == raw(r) and (not nxt or raw(y) == raw(n))
 
 
 def test_fused_call_equals_the_calls_it_replaces():
