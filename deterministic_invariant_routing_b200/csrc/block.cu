@@ -458,16 +458,18 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT)
 //   dw_next = sum_t dn r s,  dw_post = sum_t c y u
 //
 // A thread's three accumulators for each of its columns take most of its registers, so few
-// warps fit on an SM and loads have to be in flight without them: each thread copies its own
-// vectors of the next rows to its own slots of a ring in shared memory (cp.async; nobody else
-// reads them, so no barrier) and reads them back, twice, when their row comes. Rows too wide
+// warps fit on an SM and loads have to be in flight without them: each warp copies its own
+// vectors of the next rows to a ring in shared memory (cp.async, no barrier) and reads them back,
+// twice, when their row comes. Consecutive lanes copy consecutive words: of fp32, where a vector is
+// two words, a lane copies one of its own and one of another's (8192 x 2048: 76 us, 112 with
+// every lane copying its own two). Rows too wide
 // for a stage of the ring (fp32 above H = 8192) are read from memory instead.
 struct BwdRing {
     int32_t stages, arrays;               // stages 0: no ring
     int32_t i_r, i_dn, i_dr, i_y, i_gate; // place of each array in a stage, -1: absent
 };
 
-template <int DT, int V, int MAXT, int MODE>
+template <int DT, int V, int MAXT, int MODE, bool FULL>
 __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
                                                            : MAXT == 256 ? 2
                                                                          : 1)
@@ -501,7 +503,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
     // with one vector a thread its weights and channel gate stay in registers
     constexpr bool KEEP = ALL && V == 1;
     F2 kn[4], kp[4], kg[4];
-    if (KEEP) {
+    if (KEEP && (FULL || tid < nvec)) {
         load_param2<DT>(a.w_next, true, tid, kn);
         load_param2<DT>(a.w_post, true, tid, kp);
         if (gate_mode == MOE_GATE_CHANNEL) load_param2<DT>(a.gate, true, tid, kg);
@@ -511,6 +513,11 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
     // from L2: beside the ring, L1 holds less than a row's weights)
     constexpr bool SLOTS = ALL && V == 2 && MAXT != 1024;
     const uint32_t lane16 = (uint32_t)threads * 16u;
+    const int lane = tid & 31;
+    // from a lane's own place to its vector's first word (fp32: words 2 l and 2 l + 1 of 64)
+    const uint32_t own = W16 == 1 ? 0u
+                                  : (lane < 16 ? 0u : lane16) + 16u * (uint32_t)(2 * lane & 31) -
+                                        16u * (uint32_t)lane;
     const uint32_t ring0 = (uint32_t)__cvta_generic_to_shared(ring) + (uint32_t)lin * 16u;
     const uint32_t stage_bytes = (uint32_t)(g.arrays * V * W16) * lane16;
     const uint32_t slots0 = ring0 + (uint32_t)g.stages * stage_bytes;
@@ -523,10 +530,11 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
             for (int i = 0; i < V; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(
-                                     param_slot(which, i, h)),
-                                 "l"(static_cast<const uint4*>(p) + 2 * (tid + i * step) + h)
-                                 : "memory");
+                    if (FULL || tid + i * step < nvec)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(
+                                         param_slot(which, i, h)),
+                                     "l"(static_cast<const uint4*>(p) + 2 * (tid + i * step) + h)
+                                     : "memory");
         };
         stage_in(0, a.w_next);
         stage_in(1, a.w_post);
@@ -557,13 +565,13 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
             const uint4* src = static_cast<const uint4*>(p) + t * nvec * W16;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int v = tid + i * step;
-                if (ALL || v < nvec) {
 #pragma unroll
-                    for (int h = 0; h < W16; ++h)
+                for (int h = 0; h < W16; ++h) {
+                    const int word = (tid - lane + i * step) * W16 + 32 * h + lane;
+                    if (FULL || word < nvec * W16)
                         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                                          at + (uint32_t)((array * V + i) * W16 + h) * lane16),
-                                     "l"(src + v * W16 + h)
+                                     "l"(src + word)
                                      : "memory");
                 }
             }
@@ -594,7 +602,8 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
             for (int h = 0; h < W16; ++h)
                 asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                              : "=r"(w[h].x), "=r"(w[h].y), "=r"(w[h].z), "=r"(w[h].w)
-                             : "r"(at + (uint32_t)((array * V + i) * W16 + h) * lane16)
+                             : "r"(at + (uint32_t)((array * V + i) * W16) * lane16 + own +
+                                   16u * (uint32_t)h)
                              : "memory");
             q.load(w, 0);
         } else {
@@ -608,13 +617,16 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
     const F2 bscale = f2(a.branch_scale * (drop ? a.inv_keep : 1.0f));  // with 1 / P(keep)
     for (int64_t t = first; t < a.T; t += rows) {
         const int64_t row = t * nvec;
-        if (has_ring) row_ready();
+        if (has_ring) {
+            row_ready();
+            if (W16 > 1) __syncwarp();
+        }
         F2 rr = f2(0.0f), wr = f2(0.0f), yy = f2(0.0f);  // r^2, w_next dn r, y^2
         F2 kr[4], kd[4];  // KEEP: r and dn between the passes
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int v = tid + i * step;
-            if (ALL || v < nvec) {
+            if (FULL || v < nvec) {
                 F2 p[4], q[4], w[4];
                 if (next) {
                     get(at_r, a.r, row, i, p);
@@ -651,7 +663,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int v = tid + i * step;
-            if (ALL || v < nvec) {
+            if (FULL || v < nvec) {
                 F2 d[4], q[4];
                 if (has_dr) {
                     get(at_dr, a.dr, row, i, d);
@@ -746,7 +758,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int v = tid + i * step;
-                if (ALL || v < nvec) {
+                if (FULL || v < nvec) {
                     F2 y[4];
                     get(at_y, a.y, row, i, y);
 #pragma unroll
@@ -758,6 +770,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
             }
         }
         if (has_ring) {
+            if (W16 > 1) __syncwarp();  // the warp has read the stage
             fetch(at, t + g.stages * rows);
             at += stage_bytes;
             if (at == ring0 + (uint32_t)g.stages * stage_bytes) at = ring0;
@@ -990,11 +1003,11 @@ cudaError_t norm_fwd(const NormArgs& a, cudaStream_t st)
     return norm_fwd_variant<DT, 2, 1024>(a, grid, block, st);
 }
 
-template <int DT, int V, int MAXT, int MODE>
+template <int DT, int V, int MAXT, int MODE, bool FULL>
 cudaError_t norm_bwd_launch(const NormArgs& a, const BwdRing& g, dim3 grid, dim3 block, size_t smem,
                             cudaStream_t st)
 {
-    auto kernel = residual_norm_bwd_kernel<DT, V, MAXT, MODE>;
+    auto kernel = residual_norm_bwd_kernel<DT, V, MAXT, MODE, FULL>;
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
@@ -1027,13 +1040,17 @@ cudaError_t norm_bwd_variant(const NormArgs& a, BwdRing g, dim3 grid, dim3 block
     };
     g.stages = room > slots ? stages_in(room - slots) : 0;
     const bool all = a.w_post != nullptr && a.w_next != nullptr && a.dr != nullptr && a.param_f32 &&
-                     a.nvec == V * (int)block.x && g.stages > 0;
+                     g.stages > 0;
     if (!all) g.stages = stages_in(room);
     const size_t smem = g.stages * stage + (all ? slots : 0);
-    if (!all) return norm_bwd_launch<DT, V, MAXT, kAny>(a, g, grid, block, smem, st);
+    if (!all) return norm_bwd_launch<DT, V, MAXT, kAny, false>(a, g, grid, block, smem, st);
+    if (a.nvec == V * (int)block.x)
+        return a.threshold != 0
+                   ? norm_bwd_launch<DT, V, MAXT, kAllDrop, true>(a, g, grid, block, smem, st)
+                   : norm_bwd_launch<DT, V, MAXT, kAll, true>(a, g, grid, block, smem, st);
     return a.threshold != 0
-               ? norm_bwd_launch<DT, V, MAXT, kAllDrop>(a, g, grid, block, smem, st)
-               : norm_bwd_launch<DT, V, MAXT, kAll>(a, g, grid, block, smem, st);
+               ? norm_bwd_launch<DT, V, MAXT, kAllDrop, false>(a, g, grid, block, smem, st)
+               : norm_bwd_launch<DT, V, MAXT, kAll, false>(a, g, grid, block, smem, st);
 }
 
 template <int DT>

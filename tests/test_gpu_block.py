@@ -105,6 +105,27 @@ def test_residual_norm_and_backward(dt, T, H):
             check(out, g, gm, want, f"{name} {gate} {post} {p}", depth=256)
 
 
+@pytest.mark.parametrize("gate,p", [("channel", 0.2), ("channel", 0.0), ("full", 0.2),
+                                    ("token", 0.2)])
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("T,H", [(700, 128), (650, 200), (401, 400), (500, 1000), (333, 2048),
+                                 (310, 4000), (350, 6008), (12, 8192), (9, 8408)])
+def test_backward_of_the_usual_call(dt, T, H, gate, p):
+    """Both norms, fp32 parameters and dr, in rows that fill their threads and that do not."""
+    v = make(T, H, TYPES[dt], gate, seed=3)
+    rng = moe.rng_state(4, 4, device=DEV)
+    kw = dict(w_post=v["w_post"], gate=v["gate"], w_next=v["w_next"], eps=EPS,
+              residual_scale=0.75, branch_scale=1.5, p=p, rng=rng)
+    if gate == "channel":
+        kw["gate"] = v["gate"] = v["gate"].float()
+    got = moe.residual_norm_backward(v["r"], v["y"], dr=v["dr"], dn=v["dn"], **kw)
+    refs = R.backward64(d64(v["r"]), d64(v["y"]), d64(v["dr"]), d64(v["dn"]), d64(v["w_post"]),
+                        d64(v["gate"]), d64(v["w_next"]), mask_of(T, H, p, 4, 4), EPS, 0.75, 1.5)
+    assert set(got) == set(refs)
+    for name, (g, gm) in refs.items():
+        check(got[name], g, gm, got[name].dtype, name, depth=256)
+
+
 @pytest.mark.parametrize("dt", list(TYPES))
 def test_norm_alone(dt):
     """Without y: the norm before the first block, and its gradients with and without dr."""
