@@ -11,10 +11,11 @@
 // By its bytes it is bound by memory: 4 row passes forward (x, y in; r, n out), 6 backward (y,
 // r, dr, dn in; dx, dy out). A row stays in the registers of one block (one warp up to H = 512),
 // so nothing is read twice, and the backward recomputes both norms' statistics and the dropout
-// mask from what it reads anyway: nothing but r and y is kept from the forward. What bounds it
-// in fact is instructions: at 16-bit types a row pass leaves about 20 of them an element, and
-// the mask alone takes 8. Hence the packed fp32 arithmetic (F2), the kernels without branches for
-// the usual call, and the shuffles that add two values at once. Measured on B200:
+// mask from what it reads anyway: nothing but r and y is kept from the forward. What bounds the
+// backward in fact is instructions: 57 an element at 16-bit types, the mask alone 8, at 0.56 of the
+// issue rate (the copy's rate would take 0.88 of it). Hence the packed fp32 arithmetic (F2), the
+// kernels without branches for the usual call, and the shuffles that add two values at once.
+// Measured on B200:
 //   forward, 16384 x 2048 bf16, channel gate, dropout: 45 us (268 MB; 41 us at the copy's rate)
 //   backward, 8192 x 4096 bf16, the same:              97 us (403 MB; 61 us)
 //
@@ -141,9 +142,10 @@ __device__ __forceinline__ void drop2(const uint32_t (&w)[4], uint32_t threshold
 }
 
 // What a call has: kAny looks as it goes; kAll and kAllDrop are the usual call, with both norms
-// (backward: dr and room for the ring too), fp32 parameters and rows that fill their threads
-// (FULL in the kernel over many rows), without and with dropout. Bound by instructions, the looking costs: a fifth of the backward's
-// were branches and their constants.
+// (backward: dr and room for the ring too) and fp32 parameters, without and with dropout. In the
+// kernel of a block a row they also mean rows that fill their threads, elsewhere FULL says so.
+// Bound by instructions, the looking costs: a fifth of the backward's were branches and their
+// constants (16384 x 1000 bf16 90 us with it, 62 without).
 enum { kAny = 0, kAll = 1, kAllDrop = 2 };
 
 constexpr int kRowsAhead = 2;  // rows on their way in residual_norm_rows_kernel
@@ -271,8 +273,8 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT)
 // no barrier). The arithmetic is the kernel's above, value for value; a place past the row's end
 // holds zeros, which add nothing, and only its stores are left out. 16 warps an SM with 128
 // registers each and no look at the weights again: 16384 x 2048 bf16 44.8 us, against 55 for the
-// kernel above at 32 warps (8192 x 4096: 46.8 against 59).
-// (FULL: rows fill their threads; without these looks 45 us instead of 46.5.)
+// kernel above at 32 warps (8192 x 4096: 46.8 against 59). FULL: rows fill their threads (with
+// the looks at the row's end the first takes 46.5).
 template <int DT, int MAXT, int MODE, bool FULL>
 __global__ void __launch_bounds__(MAXT, 512 / MAXT)
     residual_norm_rows_kernel(const __grid_constant__ NormArgs a)
@@ -902,7 +904,7 @@ constexpr int kWarpRows = 4;  // rows of a block in the one-warp form
 // The backward: one vector a thread (its 24 sums and 24 weights in registers) up to H = 512, or in
 // fp32, where the ring leaves no room for weights in shared memory, up to H = 2048; two beyond
 // that. 16384 x 2048 with dropout and a channel gate, one vector against two: bf16 112 and 104
-// us, fp32 218 and 296.
+// us, fp32 140 and 213.
 RowShape bwd_shape(int nvec, int dtype)
 {
     if (nvec <= 32) return {true, 1, 32};

@@ -34,12 +34,11 @@
 // Measured on B200 (kernel alone, 1.9 GHz): 65536 x 4096 x 4096 in one group 375-385 us = 5.7-5.9
 // PFLOP/s (the same kernel issuing its instructions on stale operands: 315 us, 7.0); the 30B-A3B
 // layer at 16384 tokens, 128 experts: gate_up 177 us (825 GFLOP; 133 us at that rate with the
-// rounding up to tiles), down 146 us (412 GFLOP, 537 MB of output: 82 us of writing); 24594 rows
+// rounding up to tiles), down 142 us (412 GFLOP, 537 MB of output: 82 us of writing); 24594 rows
 // over 256 experts of 2048 x 4096 (1.14 GB of weights, 174 us of reading) 222 us; 512 rows over 128
-// experts of 2048 x 768 (107 MB, 16 us) 21 us. What is left
-// is the gap between two tiles of a cluster, about 1000 cycles from the last instruction of one,
-// through its epilogue's first reads, to the first of the next (the price of the shared columns),
-// and for down the stores.
+// experts of 2048 x 768 (107 MB, 16 us) 19.4 us. What is left is the gap between two tiles of a
+// cluster, about 1000 cycles from the last instruction of one, through its epilogue's first reads,
+// to the first of the next (the price of the shared columns), and for down the stores.
 #include "mx_format.cuh"
 #include "tc_common.cuh"
 

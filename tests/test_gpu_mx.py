@@ -207,6 +207,22 @@ def test_few_and_many_rows_a_group(sizes, glu):
     assert eq(one, out[lone:lone + 1])
 
 
+@pytest.mark.parametrize("groups", [320, 321, 1024])
+def test_many_groups(groups):
+    """More groups than a block has threads, empty ones and a decreasing offset among them."""
+    sizes = [(7 * i) % 5 if i % 3 else 0 for i in range(groups)]
+    sizes[-1], sizes[200] = 150, 140
+    x, w, off = make_product(sizes, 128, 128, seed=groups)
+    q, wq = moe.mx_quantize(x), moe.mx_weight(w)
+    out = moe.mx_grouped_gemm(*q, torch.tensor(off, dtype=torch.int32, device=DEV), *wq)
+    check_product(out, x, w, off, False, 128)
+    off[300] -= 1000
+    st = moe.new_status(DEV)
+    moe.mx_grouped_gemm(*q, torch.tensor(off, dtype=torch.int32, device=DEV), *wq, status=st,
+                        check=False)
+    assert st[N.MOE_ST_BAD_ROWS] > 0
+
+
 def test_nan_blocks_reach_their_results_alone():
     x, w, off = make_product([200, 100], 256, 512, seed=3)
     offs = torch.tensor(off, dtype=torch.int32, device=DEV)
