@@ -24,6 +24,7 @@
 // second kernel sums the partials in order. No atomics: the bits repeat, on any device.
 #include "fast_div.cuh"
 #include "philox.cuh"
+#include "red_layout.cuh"
 #include "vec8.cuh"
 
 namespace moe {
@@ -80,42 +81,42 @@ __device__ __forceinline__ void warp_sum(float (&v)[K])
 // Sums K values over a row's threads: within each warp, then over the warps' sums in shared
 // memory -- up to 8 of them (MAXT <= 256) added by every thread from two 16-byte reads a value,
 // which the whole warp makes at one address; more by the shuffles again. `red` (cleared by
-// red_init()) alternates between two halves, so one barrier a call is enough (a
-// warp that writes a half again has passed the barrier of the call in between, which every
-// reader of that half had reached).
-constexpr int kRed = 32;  // floats per value and half
-
-template <int K, int MAXT>
-__device__ __forceinline__ void row_sum(float (&v)[K], float* red, int& half)
+// red_init()) alternates between two halves that hold KMAX values each, the most that a kernel
+// sums at once, so that calls of different K do not meet and one barrier a call is enough
+// (red_place has the argument).
+template <int K, int KMAX, int MAXT>
+__device__ __forceinline__ void row_sum(float (&v)[K], float (&red)[kRedFloats<KMAX>], int& half)
 {
+    static_assert(K <= KMAX, "a half of the buffer holds KMAX values");
     warp_sum<K, MAXT == 32>(v);
     if (MAXT == 32) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float* b = red + half * kRed * K;
+    const int h = half;
     half ^= 1;
 #pragma unroll
     for (int k = 0; k < K; ++k)
-        if (lane == owner(k)) b[k * kRed + warp] = v[k];
+        if (lane == owner(k)) red[red_place<KMAX>(h, k, warp)] = v[k];
     __syncthreads();
     if (MAXT <= 256) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const float4 p = *reinterpret_cast<const float4*>(b + k * kRed);
-            const float4 q = *reinterpret_cast<const float4*>(b + k * kRed + 4);
+            const float4 p = *reinterpret_cast<const float4*>(red + red_place<KMAX>(h, k, 0));
+            const float4 q = *reinterpret_cast<const float4*>(red + red_place<KMAX>(h, k, 4));
             v[k] = ((p.x + p.y) + (p.z + p.w)) + ((q.x + q.y) + (q.z + q.w));
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < K; ++k) v[k] = b[k * kRed + lane];
+        for (int k = 0; k < K; ++k) v[k] = red[red_place<KMAX>(h, k, lane)];
         warp_sum<K, true>(v);
     }
 }
 
 // zeros for the warps that a block does not have (visible after row_sum's first barrier)
-__device__ __forceinline__ void red_init(float* red, int floats)
+template <int FLOATS>
+__device__ __forceinline__ void red_init(float (&red)[FLOATS])
 {
     const int warps = blockDim.x >> 5;
-    for (int i = threadIdx.x; i < floats; i += blockDim.x)
+    for (int i = threadIdx.x; i < FLOATS; i += blockDim.x)
         if ((i & (kRed - 1)) >= warps) red[i] = 0.0f;
 }
 
@@ -159,9 +160,9 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT)
     const bool post = ALL || a.w_post != nullptr, next = ALL || a.w_next != nullptr;
     const bool branch = ALL || a.y != nullptr, param_f32 = ALL || a.param_f32;
     const bool drop = MODE == kAllDrop || (MODE == kAny && a.threshold != 0);
-    __shared__ __align__(16) float red[2 * kRed];
+    __shared__ __align__(16) float red[kRedFloats<1>];
     int half = 0;
-    red_init(red, 2 * kRed);
+    red_init(red);
     pdl_wait();
     const int64_t t = ONEWARP ? (int64_t)blockIdx.x * blockDim.y + threadIdx.y : blockIdx.x;
     if (t >= a.T) return;  // whole warps (ONEWARP); never otherwise
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT)
                 }
             }
             float ss[1] = {sum2(acc)};
-            row_sum<1, MAXT>(ss, red, half);
+            row_sum<1, 1, MAXT>(ss, red, half);
             scale *= inv_rms(ss[0], a);
         }
         if (a.gate_mode == MOE_GATE_TOKEN) scale *= load_param<DT>(a.gate, param_f32, t);
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT)
         }
     }
     float ss[1] = {sum2(acc)};
-    row_sum<1, MAXT>(ss, red, half);
+    row_sum<1, 1, MAXT>(ss, red, half);
     const F2 inv = f2(inv_rms(ss[0], a));
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -285,9 +286,9 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT)
     const bool branch = ALL || a.y != nullptr, param_f32 = ALL || a.param_f32;
     const bool drop = MODE == kAllDrop || (MODE == kAny && a.threshold != 0);
     extern __shared__ uint4 ring[];
-    __shared__ __align__(16) float red[2 * kRed];
+    __shared__ __align__(16) float red[kRedFloats<1>];
     int half = 0;
-    red_init(red, 2 * kRed);
+    red_init(red);
     pdl_wait();
     const int tid = threadIdx.x, step = blockDim.x, nvec = a.nvec, gate_mode = a.gate_mode;
     const bool last_in = FULL || tid + step < nvec;  // the first vector always is
@@ -383,7 +384,7 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT)
             float scale = a.branch_scale * (drop ? a.inv_keep : 1.0f);
             if (post) {
                 ss[0] = sum2(acc);
-                row_sum<1, MAXT>(ss, red, half);
+                row_sum<1, 1, MAXT>(ss, red, half);
                 scale *= inv_rms(ss[0], a);
             }
             if (gate_mode == MOE_GATE_TOKEN) scale *= load_param<DT>(a.gate, param_f32, t);
@@ -438,7 +439,7 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT)
         if (at == end) at = base;
         if (!next) continue;
         ss[0] = sum2(acc);
-        row_sum<1, MAXT>(ss, red, half);
+        row_sum<1, 1, MAXT>(ss, red, half);
         const F2 inv = f2(inv_rms(ss[0], a));
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -480,9 +481,9 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
     constexpr bool ONEWARP = MAXT == 32, ALL = MODE != kAny;
     constexpr int W16 = DT == MOE_F32 ? 2 : 1;  // 16-byte words of a vector
     extern __shared__ uint4 ring[];
-    __shared__ __align__(16) float red[2 * kRed * 3];
+    __shared__ __align__(16) float red[kRedFloats<3>];
     int half = 0;
-    red_init(red, 2 * kRed * 3);
+    red_init(red);
     pdl_wait();
     const int tid = threadIdx.x, step = blockDim.x;
     const int lin = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
@@ -652,7 +653,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
             }
         }
         float s3[3] = {sum2(rr), sum2(wr), sum2(yy)};
-        if (next || post) row_sum<3, MAXT>(s3, red, half);
+        if (next || post) row_sum<3, 3, MAXT>(s3, red, half);
         const float s = next ? inv_rms(s3[0], a) : 0.0f;
         const F2 s2x = f2(s), mean_n = f2(next ? -s * s * s * (s3[1] * a.inv_h) : 0.0f);
         const float u = post ? inv_rms(s3[2], a) : 1.0f;
@@ -752,7 +753,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
             }
         }
         float s2[2] = {sum2(cy), sum2(bz)};
-        if (post || gate_mode == MOE_GATE_TOKEN) row_sum<2, MAXT>(s2, red, half);
+        if (post || gate_mode == MOE_GATE_TOKEN) row_sum<2, 3, MAXT>(s2, red, half);
         if (gate_mode == MOE_GATE_TOKEN && tid == 0) static_cast<float*>(a.dgate)[t] = s2[1];
         if (post) {
             // dy = u c - y u^2 mean(c y u): the sum above already holds one factor u

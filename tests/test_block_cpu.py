@@ -2,6 +2,7 @@
 published vectors, the reference gradients against central differences, and the refusals of
 the C ABI and of the binding (no GPU and no CUDA call is reached)."""
 import ctypes
+import subprocess
 
 import pytest
 import torch
@@ -200,3 +201,35 @@ def test_binding_fails_loudly_when_it_is_not_built(lib, monkeypatch, tmp_path):
     monkeypatch.setattr(N, "_binding", None)
     with pytest.raises(RuntimeError, match="not built"):
         moe.dropout(torch.zeros(2, 8), 0.5, moe.rng_state(1, device="cpu"))
+
+
+PLACES = """
+#include <stdio.h>
+#include "red_layout.cuh"
+int main()
+{
+    int half, k, warp;
+    printf("%d\\n", moe::kRedFloats<3>);
+    while (scanf("%d %d %d", &half, &k, &warp) == 3)
+        printf("%d\\n", moe::red_place<3>(half, k, warp));
+}
+"""
+
+
+@pytest.mark.parametrize("sums", [(3, 2), (3,), (2,)])
+def test_reductions_one_barrier_apart_do_not_meet(tmp_path, sums):
+    """The backward's reductions over a row's warps, `sums` values each, row after row: between
+    one call's reads and the next one's writes there is no barrier, so their places are disjoint;
+    every place is inside the buffer and a call's places are its own."""
+    (tmp_path / "places.cpp").write_text(PLACES)
+    subprocess.run(["g++", "-std=c++17", "-x", "c++", str(tmp_path / "places.cpp"), "-I",
+                    build.CSRC, "-o", str(tmp_path / "places")], check=True)
+    calls = [(i & 1, k) for i, k in enumerate(sums * 6)]
+    asked = [(h, k, w) for h, n in calls for k in range(n) for w in range(32)]
+    out = subprocess.run([str(tmp_path / "places")], check=True, text=True, capture_output=True,
+                         input="\n".join("%d %d %d" % a for a in asked)).stdout.split()
+    floats, places = int(out[0]), iter(map(int, out[1:]))
+    used = [[next(places) for _ in range(32 * n)] for _, n in calls]
+    for i, u in enumerate(used):
+        assert len(set(u)) == len(u) and min(u) >= 0 and max(u) < floats
+        assert i == 0 or not set(u) & set(used[i - 1]), (i, sums)

@@ -352,3 +352,28 @@ def test_more_than_two_to_the_31_elements():
     y = x.clone()
     moe.residual_norm(x, y, w_post=w, w_next=w, p=p, rng=rng, r=x, n=y)
     assert raw(x[-9:]) == raw(rs) and raw(y[-9:]) == raw(ns)
+
+
+@pytest.mark.parametrize("dt,H,gate", [("bf16", 520, "token"), ("bf16", 2048, "channel"),
+                                       ("f32", 1000, "token"), ("f16", 4104, "full"),
+                                       ("f32", 4096, "channel"), ("bf16", 8200, "none")])
+def test_backward_repeats_its_bits(dt, H, gate):
+    """Rows of several warps, many to a block, both reductions of each: call after call, beside
+    other work on the GPU, every output has the same bits."""
+    T = 1500
+    v = make(T, H, TYPES[dt], gate, seed=8)
+    rng = moe.rng_state(6, 6, device=DEV)
+    kw = dict(w_post=v["w_post"], gate=v["gate"], w_next=v["w_next"], eps=EPS, p=0.1, rng=rng)
+    first = moe.residual_norm_backward(v["r"], v["y"], dr=v["dr"], dn=v["dn"], **kw)
+    other, side = torch.zeros(1 << 24, device=DEV), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    differ = torch.zeros((), dtype=torch.int64, device=DEV)
+    for i in range(60):
+        if i % 2:
+            with torch.cuda.stream(side):
+                other.add_(1.0)
+        g = moe.residual_norm_backward(v["r"], v["y"], dr=v["dr"], dn=v["dn"], **kw)
+        for k, t in g.items():
+            differ += (t.view(torch.uint8) != first[k].view(torch.uint8)).sum()
+    torch.cuda.current_stream().wait_stream(side)
+    assert differ.item() == 0
