@@ -655,7 +655,9 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
         float s3[3] = {sum2(rr), sum2(wr), sum2(yy)};
         if (next || post) row_sum<3, 3, MAXT>(s3, red, half);
         const float s = next ? inv_rms(s3[0], a) : 0.0f;
-        const F2 s2x = f2(s), mean_n = f2(next ? -s * s * s * (s3[1] * a.inv_h) : 0.0f);
+        // (from the sum outwards: s^3 by itself is subnormal for rows of 1e13 and infinite for
+        // rows of zeros with an eps below 1e-25)
+        const F2 s2x = f2(s), mean_n = f2(next ? -(s * (s * (s * (s3[1] * a.inv_h)))) : 0.0f);
         const float u = post ? inv_rms(s3[2], a) : 1.0f;
         const F2 u2x = f2(u);
         const F2 tg = f2(gate_mode == MOE_GATE_TOKEN ? load_param<DT>(a.gate, param_f32, t)
@@ -757,7 +759,7 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
         if (gate_mode == MOE_GATE_TOKEN && tid == 0) static_cast<float*>(a.dgate)[t] = s2[1];
         if (post) {
             // dy = u c - y u^2 mean(c y u): the sum above already holds one factor u
-            const F2 mean_p = f2(-u * u * (s2[0] * a.inv_h));
+            const F2 mean_p = f2(-(u * (u * (s2[0] * a.inv_h))));
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int v = tid + i * step;

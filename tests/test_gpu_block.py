@@ -377,3 +377,71 @@ def test_backward_repeats_its_bits(dt, H, gate):
             differ += (t.view(torch.uint8) != first[k].view(torch.uint8)).sum()
     torch.cuda.current_stream().wait_stream(side)
     assert differ.item() == 0
+
+
+# Roundings of a row's gradients, relative to the sum of their terms' magnitudes. A row's sum takes
+# at most 8 fused adds a thread, 1 for the pair, 5 + 5 shuffles (19) and 2 for the mean; an inverse
+# root half of its argument's 22 and 4 of its own (2 ulp): 15. The mean of w dn r: 23 with its two
+# products; times three inverse roots and their products 71, times r and residual_scale 73: dx.
+# The branch's gradient has three products more and the weight (77); its mean with y u takes 17 of
+# y u and 21 of the sum (115), two inverse roots and products 147, times y 148 and one sum: dy.
+# A token's gate: 77, 18 of z, 19 of the sum.
+DEPTH = {"dx": 80, "dy": 160, "dgate": 120}
+
+
+def check_rows(got, refs, skip=()):
+    for name, (g, gm) in refs.items():
+        if name in got and name not in skip and got[name].shape[0] == refs["dx"][0].shape[0]:
+            check(got[name], g, gm, got[name].dtype, name, DEPTH[name])
+
+
+@pytest.mark.parametrize("scale", [1e13, 1e15, 1e16])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("H", [128, 512, 1000, 2048, 4104, 8200])
+def test_gradients_of_large_rows(dt, H, scale):
+    """Rows whose inverse root is far from 1 (its cube is not an fp32 number any more), with a
+    gradient along the row, so that the norm's projection is as large as the other term."""
+    v = make(7, H, TYPES[dt], "token")
+    x, y = d64(v["r"]), d64(v["y"])
+    big, wide = (x * scale).to(TYPES[dt]), (y * scale).to(TYPES[dt])
+    dn = (x + 0.1 * d64(v["dn"])).to(TYPES[dt])
+    small = (d64(v["dr"]) / scale).to(TYPES[dt])
+    for dr in (None, small):
+        kw = dict(w_post=v["w_post"], gate=v["gate"].float(), w_next=v["w_next"], eps=EPS)
+        got = moe.residual_norm_backward(big, wide, dr=dr, dn=dn, **kw)
+        refs = R.backward64(d64(big), d64(wide), d64(dr) if dr is not None else None, d64(dn),
+                            d64(v["w_post"]), d64(kw["gate"]), d64(v["w_next"]), None, EPS, 1.0,
+                            1.0)
+        check_rows({k: t for k, t in got.items() if k == "dx"}, refs)
+        alone = moe.residual_norm_backward(big, dr=dr, dn=dn, w_next=v["w_next"])
+        check_rows(alone, refs)
+        got = moe.residual_norm_backward(v["r"], wide, dr=v["dr"], dn=dn, **kw)
+        refs = R.backward64(d64(v["r"]), d64(wide), d64(v["dr"]), d64(dn), d64(v["w_post"]),
+                            d64(kw["gate"]), d64(v["w_next"]), None, EPS, 1.0, 1.0)
+        check_rows(got, refs)
+
+
+@pytest.mark.parametrize("eps", [1e-30, 1e-40])
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("H", [256, 520, 2048, 8200])
+def test_gradients_of_zero_rows_with_a_small_eps(dt, H, eps):
+    """A row of zeros has the inverse root eps^-1/2, 1e15 and more: its gradient is dn w times
+    that, with no projection, never a NaN. (fp16 holds no such gradient: dn is 0 there.)"""
+    T = 5
+    v = make(T, H, TYPES[dt], "none")
+    v["r"][2], v["y"][2] = 0, 0
+    if dt == "f16":
+        v["dn"][2], v["dr"][2] = 0, 0
+    # only dx of the row is looked at where its gradient reaches dy through another 1 / sqrt(eps)
+    got = moe.residual_norm_backward(v["r"], v["y"], dr=v["dr"], dn=v["dn"], w_post=v["w_post"],
+                                     w_next=v["w_next"], eps=eps, branch_scale=0.0)
+    eps = torch.tensor(eps, dtype=torch.float32).double().item()
+    refs = R.backward64(d64(v["r"]), d64(v["y"]), d64(v["dr"]), d64(v["dn"]), d64(v["w_post"]),
+                        None, d64(v["w_next"]), None, eps, 1.0, 0.0)
+    check_rows(got, refs, skip=("dy",))
+    assert not got["dy"].any()
+    g = moe.residual_norm_backward(v["r"], v["y"], dr=v["dr"], w_post=v["w_post"], eps=eps,
+                                   branch_scale=1e-12)
+    refs = R.backward64(d64(v["r"]), d64(v["y"]), d64(v["dr"]), None, d64(v["w_post"]), None, None,
+                        None, eps, 1.0, float(torch.tensor(1e-12)))
+    check_rows(g, refs)
