@@ -445,3 +445,21 @@ def test_gradients_of_zero_rows_with_a_small_eps(dt, H, eps):
     refs = R.backward64(d64(v["r"]), d64(v["y"]), d64(v["dr"]), None, d64(v["w_post"]), None, None,
                         None, eps, 1.0, float(torch.tensor(1e-12)))
     check_rows(g, refs)
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("T,H", SHAPES + [(700, 2048), (650, 200)])
+def test_row_gradients_within_their_own_bounds(dt, T, H):
+    """dx, dy and the gates' gradients of each row, under the roundings of a row alone (DEPTH),
+    without what the sums over tokens add."""
+    for m, (gate, post, nxt, p) in enumerate(MODES + [("token", True, True, 0.0)]):
+        v = make(T, H, TYPES[dt], gate, post, nxt, seed=40 + m,
+                 params=TYPES[dt] if m % 2 == 0 else torch.float32)
+        rng = moe.rng_state(m, 2, device=DEV)
+        got = moe.residual_norm_backward(v["r"], v["y"], dr=v["dr"], dn=v["dn"], eps=EPS,
+                                         w_post=v["w_post"], gate=v["gate"], w_next=v["w_next"],
+                                         residual_scale=0.75, branch_scale=-1.25, p=p, rng=rng)
+        refs = R.backward64(d64(v["r"]), d64(v["y"]), d64(v["dr"]), d64(v["dn"]), d64(v["w_post"]),
+                            d64(v["gate"]), d64(v["w_next"]), mask_of(T, H, p, m, 2), EPS, 0.75,
+                            -1.25)
+        check_rows(got, refs, skip=("dgate",) if gate == "channel" else ())
