@@ -76,6 +76,17 @@ void need_opt(const at::Tensor* t, const char* name, at::ScalarType dtype, at::I
     if (t != nullptr) need(t, name, dtype, shape, dev);
 }
 
+// a workspace that the caller keeps: `bytes` consecutive bytes of the device, of any type
+void need_ws(const at::Tensor& t, size_t bytes, const at::Device& dev)
+{
+    if (t.device() != dev)
+        throw Refused{"workspace on " + t.device().str() + ", expected " + dev.str()};
+    if (!t.is_contiguous()) throw Refused{"the workspace must be contiguous"};
+    if (t.nbytes() < bytes)
+        throw Refused{"workspace of " + std::to_string(t.nbytes()) + " bytes < " +
+                      std::to_string(bytes)};
+}
+
 // MOE_BF16 .. of a type, -1 of others
 int code_of(at::ScalarType t)
 {
@@ -500,20 +511,15 @@ PyObject* mx_grouped_ffn(PyObject* const* a)
         w2s = mx_weight(a[7], "w2_s", 0, c.H, c.I_shared, dev);
     }
     need_opt(status, "status", at::kInt, {MOE_STATUS_WORDS}, dev);
+    const size_t bytes = moe_workspace_bytes(&c, MOE_STAGE_MX_FFN);
+    if (given != nullptr) need_ws(*given, bytes, dev);
     need_cuda(dev);
     const auto bf16 = at::TensorOptions().dtype(at::kBFloat16).device(dev);
     const at::Tensor y = at::empty({(int64_t)c.T * c.K, c.H}, bf16);
     const at::Tensor ys = c.I_shared > 0 ? at::empty({c.T, c.H}, bf16) : at::Tensor();
-    const size_t bytes = moe_workspace_bytes(&c, MOE_STAGE_MX_FFN);
-    at::Tensor ws;
-    if (given != nullptr) {
-        if (given->nbytes() < bytes)
-            throw Refused{"workspace of " + std::to_string(given->nbytes()) + " bytes < " +
-                          std::to_string(bytes)};
-        ws = *given;
-    } else {
-        ws = at::empty({(int64_t)(bytes > 16 ? bytes : 16)}, bf16.dtype(at::kByte));
-    }
+    const at::Tensor ws =
+        given != nullptr ? *given
+                         : at::empty({(int64_t)(bytes > 16 ? bytes : 16)}, bf16.dtype(at::kByte));
     call(dev, "moe_mx_grouped_ffn", [&](void* stream) {
         return moe_mx_grouped_ffn(
             &c, static_cast<const uint16_t*>(ptr(x)), static_cast<const int32_t*>(ptr(dest)),

@@ -121,7 +121,12 @@ def check_status(status: torch.Tensor, stream_sync: bool = True):
 
 
 def _ws(nbytes: int, dev, ws: Optional[torch.Tensor]) -> torch.Tensor:
+    """The given workspace, checked, or a new one."""
     if ws is not None:
+        if ws.device != dev:
+            raise MoeError(f"workspace on {ws.device}, expected {dev}")
+        if not ws.is_contiguous():
+            raise MoeError("the workspace must be contiguous")
         if ws.numel() * ws.element_size() < nbytes:
             raise MoeError(f"workspace of {ws.numel() * ws.element_size()} bytes < {nbytes}")
         return ws

@@ -140,3 +140,39 @@ def test_binding_refusals(lib):
     for f in bad:
         with pytest.raises(moe.MoeError):
             f()
+
+
+def layer_on_the_cpu():
+    """A small layer's arguments in host memory, and the bytes of its workspaces."""
+    cfg = moe.Config(T=4, H=128, E=2, K=1, I=128)
+    x = torch.zeros(4, 128, dtype=torch.bfloat16)
+    w13 = (torch.zeros(2, 256, 64, dtype=torch.uint8), torch.zeros(2, 2, 1, 512, dtype=torch.uint8))
+    w2 = (torch.zeros(2, 128, 64, dtype=torch.uint8), torch.zeros(2, 1, 1, 512, dtype=torch.uint8))
+    dest, off = torch.zeros(4, 1, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    wr = torch.zeros(2, 128, dtype=torch.bfloat16)
+    b13, b2 = (torch.zeros(2, n, 128, dtype=torch.bfloat16) for n in (256, 128))
+    return cfg, x, w13, w2, dest, off, wr, b13, b2
+
+
+def test_workspaces_that_are_no_buffer_of_the_device_are_refused(lib):
+    """On another device than the call's tensors, strided, or expanded from fewer bytes."""
+    cfg, x, w13, w2, dest, off, wr, b13, b2 = layer_on_the_cpu()
+    n = 1 << 22
+    wrong = [torch.empty(n, dtype=torch.uint8, device="meta"),
+             torch.empty(2 * n, dtype=torch.uint8)[::2],
+             torch.empty(1, dtype=torch.uint8).expand(n)]
+    given = {"logits": torch.zeros(4, 2), "topk_ids": dest, "topk_w": torch.zeros(4, 1),
+             "dout": x}
+    for ws in wrong:
+        for f in (lambda: moe.mx_grouped_ffn(cfg, x, dest, off, w13, w2, ws=ws),
+                  lambda: moe.mx_forward(cfg, x, wr, w13, w2, ws=ws),
+                  lambda: moe.forward(cfg, x, wr, b13, b2, ws=ws),
+                  lambda: moe.forward_train(cfg, x, wr, b13, b2, ws),
+                  lambda: moe.backward(cfg, x, wr, b13, b2, *given.values(), ws=ws),
+                  lambda: moe.forward_host(cfg, x, wr, b13, b2, out_host=x, ws=ws)):
+            with pytest.raises(moe.MoeError, match="workspace"):
+                f()
+    for f in (lambda ws: moe.mx_grouped_ffn(cfg, x, dest, off, w13, w2, ws=ws),
+              lambda ws: moe.forward(cfg, x, wr, b13, b2, ws=ws)):
+        with pytest.raises(moe.MoeError, match="workspace of 16 bytes"):
+            f(torch.empty(16, dtype=torch.uint8))
