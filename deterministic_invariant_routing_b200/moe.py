@@ -112,6 +112,17 @@ def new_status(dev) -> torch.Tensor:
     return torch.zeros(N.MOE_STATUS_WORDS, dtype=torch.int32, device=dev)
 
 
+def _status(status: Optional[torch.Tensor], dev) -> torch.Tensor:
+    """The given status words, checked, or new ones."""
+    if status is None:
+        return new_status(dev)
+    if status.dtype != torch.int32 or status.device != dev or not status.is_contiguous() or \
+            status.numel() < N.MOE_STATUS_WORDS:
+        raise MoeError(f"status: {status.dtype} {tuple(status.shape)} on {status.device}, expected "
+                       f"{N.MOE_STATUS_WORDS} contiguous torch.int32 words on {dev}")
+    return status
+
+
 def check_status(status: torch.Tensor, stream_sync: bool = True):
     if stream_sync:
         torch.cuda.current_stream(status.device).synchronize()
@@ -151,7 +162,7 @@ def route(cfg: Config, x=None, w_router=None, logits=None, logit_bias=None, sel_
     _opt(token_mask, "token_mask", torch.uint8, (T,), dev)
     ids = torch.empty(T, K, dtype=torch.int32, device=dev)
     w = torch.empty(T, K, dtype=torch.float32, device=dev)
-    st = new_status(dev) if status is None else status
+    st = _status(status, dev)
     _rc(N.load().moe_route(ctypes.byref(cfg.c()), _p(x), _p(w_router), _p(logit_bias),
                            _p(sel_bias), _p(token_mask), _p(logits), _p(ids), _p(w), _p(st),
                            _stream(dev)), "moe_route")
@@ -176,7 +187,7 @@ def permute(cfg: Config, topk_ids, x=None, want_x_perm: bool = True, status=None
         x_perm = torch.empty(T * K, H, dtype=torch.bfloat16, device=dev)
     nbytes = workspace_bytes(cfg, N.MOE_STAGE_PERMUTE)
     ws = _ws(nbytes, dev, None)
-    st = new_status(dev) if status is None else status
+    st = _status(status, dev)
     _rc(N.load().moe_permute(ctypes.byref(cfg.c()), _p(topk_ids), _p(x), _p(offsets),
                              _p(perm_token), _p(dest_row), _p(x_perm), _p(st), _p(ws),
                              ws.numel(), _stream(dev)), "moe_permute")
@@ -202,7 +213,7 @@ def grouped_ffn(cfg: Config, x, x_perm, perm_token, offsets, w13, w2, w13_s=None
     y = torch.empty(T * K, H, dtype=torch.bfloat16, device=dev)
     y_s = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if Is else None
     ws = _ws(workspace_bytes(cfg, N.MOE_STAGE_FFN), dev, None)
-    st = new_status(dev) if status is None else status
+    st = _status(status, dev)
     _rc(N.load().moe_grouped_ffn(ctypes.byref(cfg.c()), _p(x), _p(x_perm), _p(perm_token),
                                  _p(offsets), _p(w13), _p(w2), _p(w13_s), _p(w2_s), _p(y),
                                  _p(y_s), _p(st), _p(ws), ws.numel(), _stream(dev)),
@@ -364,7 +375,7 @@ def forward_train(cfg: Config, x, w_router, w13, w2, ws, logit_bias=None, sel_bi
          "topk_w": torch.empty(T, K, dtype=torch.float32, device=dev)}
     nbytes = workspace_bytes(cfg, N.MOE_STAGE_BACKWARD)
     ws = _ws(nbytes, dev, ws)
-    st = new_status(dev) if status is None else status
+    st = _status(status, dev)
     _rc(N.load().moe_forward_train(ctypes.byref(cfg.c()), _p(x), _p(w_router), _p(logit_bias),
                                    _p(sel_bias), _p(token_mask), _p(w13), _p(w2), _p(w13_s),
                                    _p(w2_s), _p(out), _p(b["logits"]), _p(b["topk_ids"]),
@@ -410,7 +421,7 @@ def backward(cfg: Config, x, w_router, w13, w2, logits, topk_ids, topk_w, dout, 
         g["dlogits"] = torch.empty(T, E, dtype=torch.float32, device=dev)
     nbytes = workspace_bytes(cfg, N.MOE_STAGE_BACKWARD)
     ws = _ws(nbytes, dev, ws)
-    st = new_status(dev) if status is None else status
+    st = _status(status, dev)
     _rc(N.load().moe_backward(ctypes.byref(cfg.c()), _p(x), _p(w_router), _p(token_mask),
                               _p(w13), _p(w2), _p(w13_s), _p(w2_s), _p(logits), _p(topk_ids),
                               _p(topk_w), _p(dout), _p(g["dx"]), _p(g["dw_router"]),
@@ -447,7 +458,7 @@ def forward(cfg: Config, x, w_router, w13, w2, logit_bias=None, sel_bias=None, t
     out = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if out is None else out
     _need(out, "out", torch.bfloat16, (T, H), dev)
     ws = _ws(workspace_bytes(cfg, N.MOE_STAGE_FORWARD), dev, ws)
-    st = new_status(dev) if status is None else status
+    st = _status(status, dev)
     b = {}
     if keep:
         b = {"logits": torch.empty(T, E, dtype=torch.float32, device=dev),
@@ -502,7 +513,7 @@ def forward_host(cfg: Config, x_host, w_router, w13, w2, logit_bias=None, sel_bi
         _need(w13_s, "w13_s", torch.bfloat16, (2 * Is, H), dev)
         _need(w2_s, "w2_s", torch.bfloat16, (H, Is), dev)
     ws = _ws(forward_host_workspace_bytes(cfg, chunk), dev, ws)
-    st = new_status(dev) if status is None else status
+    st = _status(status, dev)
     _rc(N.load().moe_forward_host(ctypes.byref(cfg.c()), _p(x_host), _p(w_router),
                                   _p(logit_bias), _p(sel_bias), _p(token_mask), _p(w13), _p(w2),
                                   _p(w13_s), _p(w2_s), _p(out_host), _p(st), int(chunk), _p(ws),
@@ -612,7 +623,7 @@ def mx_forward(cfg: Config, x, w_router, w13, w2, logit_bias=None, sel_bias=None
     lib, ref = N.load(), ctypes.byref(cfg.c())
     nbytes = lib.moe_workspace_bytes(ref, N.MOE_STAGE_MX_FORWARD)
     ws = _ws(nbytes, dev, ws)
-    st = new_status(dev) if status is None else status
+    st = _status(status, dev)
     b = {}
     if keep:
         b = {"logits": torch.empty(T, E, dtype=torch.float32, device=dev),

@@ -176,3 +176,29 @@ def test_workspaces_that_are_no_buffer_of_the_device_are_refused(lib):
               lambda ws: moe.forward(cfg, x, wr, b13, b2, ws=ws)):
         with pytest.raises(moe.MoeError, match="workspace of 16 bytes"):
             f(torch.empty(16, dtype=torch.uint8))
+
+
+def test_status_words_that_are_no_buffer_of_the_device_are_refused(lib):
+    """On another device, of another type, too few, strided or expanded."""
+    cfg, x, w13, w2, dest, off, wr, b13, b2 = layer_on_the_cpu()
+    n = N.MOE_STATUS_WORDS
+    wrong = [torch.zeros(n, dtype=torch.int32, device="meta"), torch.zeros(n),
+             torch.zeros(n, dtype=torch.int64), torch.zeros(n - 1, dtype=torch.int32),
+             torch.zeros(2 * n, dtype=torch.int32)[::2],
+             torch.zeros(1, dtype=torch.int32).expand(n)]
+    lg, tw = torch.zeros(4, 2), torch.zeros(4, 1)
+    for st in wrong:
+        for f in (lambda: moe.mx_forward(cfg, x, wr, w13, w2, status=st),
+                  lambda: moe.mx_grouped_ffn(cfg, x, dest, off, w13, w2, status=st),
+                  lambda: moe.mx_grouped_gemm(x.view(torch.uint8)[:, :64].contiguous(),
+                                              w13[1][0, :1].contiguous(), off, *w13, status=st),
+                  lambda: moe.route(cfg, x, wr, status=st),
+                  lambda: moe.permute(cfg, dest, x, status=st),
+                  lambda: moe.grouped_ffn(cfg, x, x, dest.view(-1), off, b13, b2, status=st),
+                  lambda: moe.forward(cfg, x, wr, b13, b2, status=st),
+                  lambda: moe.forward_train(cfg, x, wr, b13, b2,
+                                            torch.empty(1 << 22, dtype=torch.uint8), status=st),
+                  lambda: moe.backward(cfg, x, wr, b13, b2, lg, dest, tw, x, status=st),
+                  lambda: moe.forward_host(cfg, x, wr, b13, b2, out_host=x, status=st)):
+            with pytest.raises(moe.MoeError, match="status"):
+                f()
