@@ -462,10 +462,16 @@ PyObject* mx_grouped_gemm(PyObject* const* a)
     return wrap(out);
 }
 
-// (codes, tiled scales) of matrices [n, k], `lead` of them (0: one, without the dimension)
+// (codes, tiled scales) of matrices [n, k], `lead` of them (0: one, without the dimension), held:
+// a sequence may make its members when asked, and then nothing else refers to them
 struct MxWeight {
-    const uint8_t *codes, *scales;
+    at::Tensor codes, scales;
 };
+
+const uint8_t* bytes_of(const at::Tensor& t)  // NULL for none
+{
+    return t.defined() ? static_cast<const uint8_t*>(t.const_data_ptr()) : nullptr;
+}
 
 MxWeight mx_weight(PyObject* o, const char* name, int64_t lead, int64_t n, int64_t k,
                    const at::Device& dev)
@@ -476,11 +482,13 @@ MxWeight mx_weight(PyObject* o, const char* name, int64_t lead, int64_t n, int64
         Py_XDECREF(s);
         throw Refused{std::string(name) + ": (codes, scales) of mx_weight() are expected"};
     }
-    PyObject* const c = PySequence_Fast_GET_ITEM(s, 0);
-    PyObject* const t = PySequence_Fast_GET_ITEM(s, 1);
-    Py_DECREF(s);  // o still holds both
+    struct Release {
+        PyObject* o;
+        ~Release() { Py_DECREF(o); }
+    } const release{s};
     const std::string cn = std::string(name) + " codes", sn = std::string(name) + " scales";
-    const at::Tensor *codes = tensor(c, cn.c_str()), *scales = tensor(t, sn.c_str());
+    const at::Tensor *codes = tensor(PySequence_Fast_GET_ITEM(s, 0), cn.c_str());
+    const at::Tensor *scales = tensor(PySequence_Fast_GET_ITEM(s, 1), sn.c_str());
     if (lead > 0) {
         need(codes, cn.c_str(), at::kByte, {lead, n, k / 2}, dev);
         need(scales, sn.c_str(), at::kByte, {lead, n / 128, k / 128, 512}, dev);
@@ -488,7 +496,7 @@ MxWeight mx_weight(PyObject* o, const char* name, int64_t lead, int64_t n, int64
         need(codes, cn.c_str(), at::kByte, {n, k / 2}, dev);
         need(scales, sn.c_str(), at::kByte, {n / 128, k / 128, 512}, dev);
     }
-    return {static_cast<const uint8_t*>(ptr(codes)), static_cast<const uint8_t*>(ptr(scales))};
+    return {*codes, *scales};
 }
 
 // cfg, x, dest_row, offsets, w13, w2, w13_s, w2_s, ws, status
@@ -505,7 +513,7 @@ PyObject* mx_grouped_ffn(PyObject* const* a)
     need(offsets, "offsets", at::kInt, {(int64_t)c.E + 1}, dev);
     const MxWeight w13 = mx_weight(a[4], "w13", c.E, 2 * (int64_t)c.I, c.H, dev);
     const MxWeight w2 = mx_weight(a[5], "w2", c.E, c.H, c.I, dev);
-    MxWeight w13s{nullptr, nullptr}, w2s{nullptr, nullptr};
+    MxWeight w13s, w2s;
     if (c.I_shared > 0) {
         w13s = mx_weight(a[6], "w13_s", 0, 2 * (int64_t)c.I_shared, c.H, dev);
         w2s = mx_weight(a[7], "w2_s", 0, c.H, c.I_shared, dev);
@@ -523,8 +531,9 @@ PyObject* mx_grouped_ffn(PyObject* const* a)
     call(dev, "moe_mx_grouped_ffn", [&](void* stream) {
         return moe_mx_grouped_ffn(
             &c, static_cast<const uint16_t*>(ptr(x)), static_cast<const int32_t*>(ptr(dest)),
-            static_cast<const int32_t*>(ptr(offsets)), w13.codes, w13.scales, w2.codes, w2.scales,
-            w13s.codes, w13s.scales, w2s.codes, w2s.scales, static_cast<uint16_t*>(out_ptr(y)),
+            static_cast<const int32_t*>(ptr(offsets)), bytes_of(w13.codes), bytes_of(w13.scales),
+            bytes_of(w2.codes), bytes_of(w2.scales), bytes_of(w13s.codes), bytes_of(w13s.scales),
+            bytes_of(w2s.codes), bytes_of(w2s.scales), static_cast<uint16_t*>(out_ptr(y)),
             static_cast<uint16_t*>(out_ptr(ys)),
             static_cast<int32_t*>(status == nullptr ? nullptr : status->data_ptr()), out_ptr(ws),
             bytes, stream);

@@ -562,8 +562,9 @@ def _mx_need(w, name, n, k, dev, lead=()):
     """4-bit weights (codes, tiled scales) of matrices [n, k], lead = (how many,) or ()."""
     if w is None or len(w) != 2:
         raise MoeError(f"{name}: (codes, scales) of mx_weight() are expected")
-    _need(w[0], f"{name} codes", torch.uint8, lead + (n, k // 2), dev)
-    _need(w[1], f"{name} scales", torch.uint8, lead + (n // 128, k // 128, 512), dev)
+    codes, scales = w  # once: a sequence may make its members when asked
+    return (_need(codes, f"{name} codes", torch.uint8, lead + (n, k // 2), dev),
+            _need(scales, f"{name} scales", torch.uint8, lead + (n // 128, k // 128, 512), dev))
 
 
 def mx_grouped_gemm(codes, scales, offsets, w_codes, w_scales, swiglu: bool = False, out=None,
@@ -580,16 +581,12 @@ def mx_grouped_gemm(codes, scales, offsets, w_codes, w_scales, swiglu: bool = Fa
 
 
 def _mx_experts(cfg, w13, w2, w13_s, w2_s, dev):
-    """The pointers of a layer's 4-bit expert weights, checked."""
+    """The tensors of a layer's 4-bit expert weights, checked, in the order of the C ABI."""
     H, I, Is, E = cfg.H, cfg.I, cfg.I_shared, (cfg.E,)
-    _mx_need(w13, "w13", 2 * I, H, dev, E)
-    _mx_need(w2, "w2", H, I, dev, E)
-    p = (w13[0].data_ptr(), w13[1].data_ptr(), w2[0].data_ptr(), w2[1].data_ptr())
+    w = _mx_need(w13, "w13", 2 * I, H, dev, E) + _mx_need(w2, "w2", H, I, dev, E)
     if not Is:
-        return p + (None, None, None, None)
-    _mx_need(w13_s, "w13_s", 2 * Is, H, dev)
-    _mx_need(w2_s, "w2_s", H, Is, dev)
-    return p + (w13_s[0].data_ptr(), w13_s[1].data_ptr(), w2_s[0].data_ptr(), w2_s[1].data_ptr())
+        return w + (None, None, None, None)
+    return w + _mx_need(w13_s, "w13_s", 2 * Is, H, dev) + _mx_need(w2_s, "w2_s", H, Is, dev)
 
 
 def mx_grouped_ffn(cfg: Config, x, dest_row, offsets, w13, w2, w13_s=None, w2_s=None, ws=None,
@@ -631,9 +628,9 @@ def mx_forward(cfg: Config, x, w_router, w13, w2, logit_bias=None, sel_bias=None
              "topk_w": torch.empty(T, K, dtype=torch.float32, device=dev),
              "offsets": torch.empty(E + 1, dtype=torch.int32, device=dev)}
     _rc(_call(dev, lib.moe_mx_forward, ref, _p(x), _p(w_router),
-              _p(logit_bias), _p(sel_bias), _p(token_mask), *w, _p(out), _p(b.get("logits")),
-              _p(b.get("topk_ids")), _p(b.get("topk_w")), _p(b.get("offsets")), _p(st), _p(ws),
-              nbytes), "moe_mx_forward")
+              _p(logit_bias), _p(sel_bias), _p(token_mask), *map(_p, w), _p(out),
+              _p(b.get("logits")), _p(b.get("topk_ids")), _p(b.get("topk_w")),
+              _p(b.get("offsets")), _p(st), _p(ws), nbytes), "moe_mx_forward")
     if check:
         check_status(st)
     return (out, b) if keep else out

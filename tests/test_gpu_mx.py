@@ -410,3 +410,30 @@ def test_layer_replayed_from_a_graph_and_on_two_streams():
     torch.cuda.synchronize()
     for i, o in enumerate(outs):
         assert eq(o, want[i // 5])
+
+
+class MadeWhenAsked:
+    """Weights of mx_weight() as a sequence that makes its members anew each time."""
+
+    def __init__(self, pair):
+        self.pair = [t.cpu() for t in pair]
+
+    def __len__(self):
+        return 2
+
+    def __getitem__(self, i):
+        return self.pair[i].to(DEV)
+
+
+def test_weights_from_a_sequence_are_held_through_the_call():
+    """Nothing but the call refers to the members: their memory is not taken by its outputs."""
+    cfg = moe.Config(T=70, H=256, E=4, K=2, I=128)
+    x, wr = rows_like((70, 256), 1), rows_like((4, 256), 2)
+    w13, w2 = moe.mx_weight(rows_like((4, 256, 256), 3)), moe.mx_weight(rows_like((4, 256, 128), 4))
+    want, b = moe.mx_forward(cfg, x, wr, w13, w2, keep=True)
+    got, _ = moe.mx_forward(cfg, x, wr, MadeWhenAsked(w13), MadeWhenAsked(w2), keep=True)
+    assert eq(got, want)
+    offsets, _, dest, _ = moe.permute(cfg, b["topk_ids"], want_x_perm=False)
+    y, _ = moe.mx_grouped_ffn(cfg, x, dest, offsets, w13, w2)
+    y2, _ = moe.mx_grouped_ffn(cfg, x, dest, offsets, MadeWhenAsked(w13), MadeWhenAsked(w2))
+    assert eq(y, y2)

@@ -1,6 +1,9 @@
 """CPU checks of the 4-bit experts: the reference format by hand-worked values, the scale tiles,
 and the refusals of the C ABI and the binding."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -202,3 +205,38 @@ def test_status_words_that_are_no_buffer_of_the_device_are_refused(lib):
                   lambda: moe.forward_host(cfg, x, wr, b13, b2, out_host=x, status=st)):
             with pytest.raises(moe.MoeError, match="status"):
                 f()
+
+
+HELD = """
+import gc, sys
+import torch
+from deterministic_invariant_routing_b200 import moe
+cfg = moe.Config(T=4, H=128, E=2, K=1, I=128)
+
+class Weights:  # a sequence that makes its members when asked
+    def __init__(self, n, k): self.n, self.k = n, k
+    def __len__(self): return 2
+    def __getitem__(self, i):
+        if i > 1: raise IndexError(i)
+        if i == 0: return torch.zeros(2, self.n, self.k // 2, dtype=torch.uint8)
+        return torch.zeros(2, self.n // 128, self.k // 128, 512, dtype=torch.uint8)
+
+x = torch.zeros(4, 128, dtype=torch.bfloat16)
+dest, off = torch.zeros(4, 1, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+for _ in range(50):
+    try:
+        moe.mx_grouped_ffn(cfg, x, dest, off, Weights(256, 128), Weights(128, 128))
+    except moe.MoeError as e:
+        assert "tensors on cpu" in str(e), e
+    else:
+        sys.exit("not refused")
+print("held")
+"""
+
+
+def test_weights_from_a_sequence_are_held_through_the_call(lib):
+    """Members that only the call refers to: their shapes are read, and in a call on the GPU
+    their memory is used, after the sequence's list of them is gone."""
+    r = subprocess.run([sys.executable, "-c", HELD], capture_output=True, text=True,
+                       cwd=os.path.dirname(build.PKG), env=dict(os.environ, PYTHONMALLOC="debug"))
+    assert r.returncode == 0 and "held" in r.stdout, (r.returncode, r.stderr[-2000:])
