@@ -28,8 +28,9 @@
 // of 128 columns), one accumulator; nothing depends on where the row sits, on its expert's
 // other rows or on T. Rows outside the group are computed and never stored.
 //
-// Every wait is bounded (MOE_ST_PIPE_TIMEOUT); offsets outside [0, rows] are clamped and counted
-// in MOE_ST_BAD_ROWS, so no tile reaches past the buffers.
+// Every wait is bounded (MOE_ST_PIPE_TIMEOUT); offsets outside [0, rows] or below the largest
+// before them are clamped and counted in MOE_ST_BAD_ROWS, so no tile reaches past the buffers and
+// no row is in two groups.
 //
 // Measured on B200 (kernel alone, 1.9 GHz): 65536 x 4096 x 4096 in one group 375-385 us = 5.7-5.9
 // PFLOP/s (the same kernel issuing its instructions on stale operands: 315 us, 7.0); the 30B-A3B
@@ -318,16 +319,17 @@ __global__ void __launch_bounds__(kXThreads, 1)
     // The groups' offsets, clamped, and the row tiles before each group: a group a thread, scanned
     // within a warp and then over the warps' totals. (Offsets by all threads and then four groups
     // a lane of one warp took 1600 cycles at 128 groups, of the 20 000 of a decode product.)
-    int carry = 0;
+    int carry = 0, falling = 0;  // falling: some offset is below its predecessor
     for (int g0 = 0; g0 < G; g0 += kXThreads) {
         const int g = g0 + (int)threadIdx.x;
-        int n = 0;
+        int n = 0, falls = 0;
         if (g < G) {
             const int rows = (int)args.rows;
             const int raw0 = args.offsets != nullptr ? args.offsets[g] : 0;
             const int raw1 = args.offsets != nullptr ? args.offsets[g + 1] : rows;
             const int beg = min(max(raw0, 0), rows), end = min(max(raw1, 0), rows);
             n = mx_row_tiles(beg, end, XM);
+            falls = end < beg;
             offs[g] = beg;
             if (g == G - 1) offs[G] = end;
             if (blockIdx.x == 0) {
@@ -343,7 +345,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         }
         if (g0 != 0) __syncthreads();  // the totals of the 320 groups before are read
         if (lane == 31) totals[warp] = incl;
-        __syncthreads();
+        falling |= __syncthreads_or(falls);
         int before = 0, all = 0;
 #pragma unroll
         for (int w = 0; w < kXThreads / 32; ++w) {
@@ -353,6 +355,25 @@ __global__ void __launch_bounds__(kXThreads, 1)
         }
         if (g < G) prefix[g] = carry + before + incl - n;
         carry += all;
+    }
+    if (falling) {
+        // every offset is raised to the largest before it, so that no row is in two groups (two
+        // tiles would store it in no order); counted above, and not in a hurry
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            int top = offs[0], tiles = 0;
+            for (int g = 0; g < G; ++g) {
+                const int end = max(offs[g + 1], top);
+                offs[g] = top;
+                prefix[g] = tiles;
+                tiles += mx_row_tiles(top, end, XM);
+                top = end;
+            }
+            offs[G] = top;
+            totals[0] = tiles;
+        }
+        __syncthreads();
+        carry = totals[0];
     }
     if (threadIdx.x == 0) prefix[G] = carry;
     tc_fence_before();

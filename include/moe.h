@@ -522,7 +522,8 @@ MOE_API int moe_mx_dequantize(int64_t rows, int32_t K, int32_t dtype, int32_t ti
  *
  *  a_codes [rows, K / 2], a_scales in tiles  (from moe_mx_quantize).
  *  offsets  [groups + 1] int32 device, or NULL (groups = 1: all rows). An offset outside
- *           [0, rows] or below its predecessor counts in status[MOE_ST_BAD_ROWS] and is clamped.
+ *           [0, rows] or below its predecessor counts in status[MOE_ST_BAD_ROWS]; it is clamped
+ *           to [0, rows] and raised to the largest offset before it, so no row is in two groups.
  *  b_codes  [groups, N, K / 2], b_scales in tiles, [groups, N / 128, K / 128, 512].
  *  out      [rows, N] bf16, or [rows, N / 2] with swiglu.
  *  status   int32[MOE_STATUS_WORDS] device, cleared first; may be NULL.

@@ -437,3 +437,49 @@ def test_weights_from_a_sequence_are_held_through_the_call():
     y, _ = moe.mx_grouped_ffn(cfg, x, dest, offsets, w13, w2)
     y2, _ = moe.mx_grouped_ffn(cfg, x, dest, offsets, MadeWhenAsked(w13), MadeWhenAsked(w2))
     assert eq(y, y2)
+
+
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("bad", [[0, 40, 30, 60], [0, 300, 10, 500], [0, 300, -5, 500],
+                                 [200, 600, 100, 350], [0, 900, 0, 600], [900, 40, 20, 10],
+                                 [0, 128, 100, 260], [0, 10, 5, 7]])
+def test_falling_offsets_give_the_clamped_groups(bad, glu):
+    """Every offset clamped to the rows and raised to the largest before it: the results of those
+    offsets, bit for bit and again, rows outside them as they were, and one count or more."""
+    n, K, R = 512, 256, 600
+    x, w = rows_like((R, K), 11), moe.mx_weight(rows_like((3, n, K), 12) * 0.02)
+    q = moe.mx_quantize(x)
+    good, top = [], 0
+    for o in bad:
+        top = max(top, min(max(o, 0), R))
+        good.append(top)
+
+    def run(off):
+        out, st = torch.full((R, n // (1 + glu)), 3.0, dtype=torch.bfloat16, device=DEV), \
+            moe.new_status(DEV)
+        moe.mx_grouped_gemm(*q, torch.tensor(off, dtype=torch.int32, device=DEV), *w, swiglu=glu,
+                            out=out, status=st, check=False)
+        return out, st.tolist()
+
+    want, clean = run(good)
+    assert not any(clean)
+    for _ in range(3):
+        got, st = run(bad)
+        assert eq(got, want) and st[N.MOE_ST_BAD_ROWS] > 0
+        assert not any(v for i, v in enumerate(st) if i != N.MOE_ST_BAD_ROWS)
+
+
+def test_falling_offsets_among_many_groups():
+    """More groups than a block has threads, offsets that fall at several places among them."""
+    groups, R = 700, 2000
+    x, w = rows_like((R, 128), 13), moe.mx_weight(rows_like((groups, 128, 128), 14))
+    q = moe.mx_quantize(x)
+    off = [3 * g - (400 if g % 97 == 50 else 0) for g in range(groups)] + [R]
+    good, top = [], 0
+    for o in off:
+        top = max(top, min(max(o, 0), R))
+        good.append(top)
+    a, b = (moe.mx_grouped_gemm(*q, torch.tensor(o, dtype=torch.int32, device=DEV), *w,
+                                out=torch.zeros(R, 128, dtype=torch.bfloat16, device=DEV),
+                                check=False) for o in (off, good))
+    assert eq(a, b)
