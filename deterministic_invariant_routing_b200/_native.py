@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 import threading
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -134,6 +135,19 @@ def load():
 _binding = None
 
 
+def binding_target() -> str:
+    """What the native part of the binding is compiled against, besides its sources."""
+    import torch
+    return f"torch {torch.__version__}, Python {sys.version_info[0]}.{sys.version_info[1]}"
+
+
+def binding_built_for() -> str:
+    """binding_target() of the native part's build, which it carries as text ("" if it does not)."""
+    with open(BINDING_PATH, "rb") as f:
+        _, mark, rest = f.read().partition(b"moe_binding built for ")
+    return rest.partition(b"\0")[0].decode() if mark else ""
+
+
 def load_binding(error):
     """The native part of the binding (csrc/binding.cpp), raising `error` for what it refuses."""
     global _binding
@@ -144,6 +158,11 @@ def load_binding(error):
                 raise RuntimeError(
                     f"moe_binding.so is not built ({BINDING_PATH}); run "
                     "`python -m deterministic_invariant_routing_b200.build` (needs nvcc and g++)")
+            if binding_built_for() != binding_target():
+                raise RuntimeError(
+                    f"moe_binding.so was built for {binding_built_for() or 'an unknown torch'}, "
+                    f"this is {binding_target()}; run "
+                    "`python -m deterministic_invariant_routing_b200.build`")
             import importlib.machinery
             import importlib.util
             loader = importlib.machinery.ExtensionFileLoader("moe_binding", BINDING_PATH)

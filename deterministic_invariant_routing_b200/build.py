@@ -12,6 +12,8 @@ import shutil
 import subprocess
 import sys
 
+from ._native import BINDING_PATH, binding_built_for, binding_target
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
@@ -20,7 +22,6 @@ LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libmoe_b200.so")
 HEADER = os.path.join(ROOT, "include", "moe.h")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
-BINDING_PATH = os.path.join(LIB_DIR, "moe_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -51,7 +52,7 @@ def up_to_date() -> bool:
 
 
 def _binding_up_to_date() -> bool:
-    if not os.path.exists(BINDING_PATH):
+    if not os.path.exists(BINDING_PATH) or binding_built_for() != binding_target():
         return False
     t = os.path.getmtime(BINDING_PATH)
     return all(os.path.getmtime(p) <= t for p in (BINDING_SRC, HEADER))
@@ -73,6 +74,7 @@ def _build_binding() -> None:
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DMOE_BINDING_TARGET="{binding_target()}"',
            *[f for d in inc for f in ("-isystem", d)], BINDING_SRC, "-o", tmp, "-L", LIB_DIR,
            "-l:libmoe_b200.so", "-L", libs, "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10",
            "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]

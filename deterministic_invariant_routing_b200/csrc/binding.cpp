@@ -586,4 +586,9 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "moe_binding", nullptr, -1, kMetho
 
 }  // namespace
 
+// what this file was compiled against (a macro of the build), read from the built file before it is
+// loaded: another torch's C++ interface is not this one's
+extern "C" __attribute__((used, visibility("default"))) const char moe_binding_built_for[] =
+    "moe_binding built for " MOE_BINDING_TARGET;
+
 PyMODINIT_FUNC PyInit_moe_binding(void) { return PyModule_Create(&kModule); }

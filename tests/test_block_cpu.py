@@ -233,3 +233,18 @@ def test_reductions_one_barrier_apart_do_not_meet(tmp_path, sums):
     for i, u in enumerate(used):
         assert len(set(u)) == len(u) and min(u) >= 0 and max(u) < floats
         assert i == 0 or not set(u) & set(used[i - 1]), (i, sums)
+
+
+def test_binding_of_another_torch_is_rebuilt_and_not_loaded(lib, monkeypatch):
+    """The binding is compiled against torch's C++ headers: another version's is out of date for
+    the build, and loading it is refused with what to do."""
+    assert build._binding_up_to_date()
+    monkeypatch.setattr(torch, "__version__", "1.0.0+other")
+    assert not build._binding_up_to_date()
+    monkeypatch.setattr(N, "_binding", None)
+    with pytest.raises(RuntimeError, match="other.*build"):
+        moe.dropout(torch.zeros(2, 8), 0.5, moe.rng_state(1, device="cpu"))
+    monkeypatch.undo()
+    assert build._binding_up_to_date()
+    with pytest.raises(moe.MoeError):  # loaded, and refuses the host's tensors
+        moe.dropout(torch.zeros(2, 8), 0.5, moe.rng_state(1, device="cpu"))
