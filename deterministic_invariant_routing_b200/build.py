@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -58,6 +59,15 @@ def _binding_up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in (BINDING_SRC, HEADER))
 
 
+def _refresh_binding(force: bool = False) -> None:
+    """Build the binding if it is out of date. It is a torch extension: without torch there is
+    nothing to bind, and the library, which needs nvcc alone, stands by itself."""
+    if importlib.util.find_spec("torch") is None:
+        sys.stderr.write("torch not found: libmoe_b200.so is built without moe_binding.so\n")
+    elif force or not _binding_up_to_date():
+        _build_binding()
+
+
 def _build_binding() -> None:
     import sysconfig
 
@@ -96,11 +106,10 @@ def _compile(src: str, extra) -> str:
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile every kernel for sm_100a and link the shared library, then the binding. Returns the
-    library's path."""
+    """Compile every kernel for sm_100a and link the shared library, then the binding (where torch
+    is installed). Returns the library's path."""
     if not force and not verbose_ptxas and up_to_date():
-        if not _binding_up_to_date():
-            _build_binding()
+        _refresh_binding()
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
@@ -114,8 +123,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
-    if force or not _binding_up_to_date():
-        _build_binding()
+    _refresh_binding(force)
     return LIB_PATH
 
 

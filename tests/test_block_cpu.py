@@ -2,7 +2,9 @@
 published vectors, the reference gradients against central differences, and the refusals of
 the C ABI and of the binding (no GPU and no CUDA call is reached)."""
 import ctypes
+import importlib.util
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -248,3 +250,16 @@ def test_binding_of_another_torch_is_rebuilt_and_not_loaded(lib, monkeypatch):
     assert build._binding_up_to_date()
     with pytest.raises(moe.MoeError):  # loaded, and refuses the host's tensors
         moe.dropout(torch.zeros(2, 8), 0.5, moe.rng_state(1, device="cpu"))
+
+
+def test_the_library_builds_without_torch(lib, monkeypatch, capsys):
+    """The kernels' library needs nvcc alone, for whoever calls the C ABI: without torch the
+    binding, which is torch's, is left out with a note."""
+    find = importlib.util.find_spec
+    monkeypatch.setattr(importlib.util, "find_spec",
+                        lambda name, *a: None if name == "torch" else find(name, *a))
+    monkeypatch.setitem(sys.modules, "torch", None)  # import torch raises ImportError
+    assert build.build() == build.LIB_PATH
+    assert "without moe_binding.so" in capsys.readouterr().err
+    monkeypatch.undo()
+    assert build._binding_up_to_date()
