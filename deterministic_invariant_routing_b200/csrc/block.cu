@@ -11,13 +11,18 @@
 // By its bytes it is bound by memory: 4 row passes forward (x, y in; r, n out), 6 backward (y,
 // r, dr, dn in; dx, dy out). A row stays in the registers of one block (one warp up to H = 512),
 // so nothing is read twice, and the backward recomputes both norms' statistics and the dropout
-// mask from what it reads anyway: nothing but r and y is kept from the forward. What bounds the
-// backward in fact is instructions: 57 an element at 16-bit types, the mask alone 8, at 0.56 of the
-// issue rate (the copy's rate would take 0.88 of it). Hence the packed fp32 arithmetic (F2), the
-// kernels without branches for the usual call, and the shuffles that add two values at once.
-// Measured on B200:
+// mask from what it reads anyway: nothing but r and y is kept from the forward. The backward does
+// not reach that bound, nor another: at 16-bit types it has 57 instructions an element, the mask
+// alone 8, and issues at 0.57 of the rate (memory at the copy's rate would take 0.88 of it) with 16
+// warps an SM, all that the sums of the parameter gradients allow; latency is left, around a row's
+// two barriers. Instructions are what there was to take out: hence the packed fp32 arithmetic
+// (F2), the kernels without branches for calls with both norms, and the shuffles that add two values
+// at once. Measured on B200:
 //   forward, 16384 x 2048 bf16, channel gate, dropout: 45 us (268 MB; 41 us at the copy's rate)
-//   backward, 8192 x 4096 bf16, the same:              97 us (403 MB; 61 us)
+//   forward, the same without w_post, gate and dropout, bf16 weights: 47.5 us
+//   backward, 8192 x 4096 bf16, channel gate, dropout: 97 us (403 MB; 61 us)
+//   backward, 16384 x 2048 bf16, both norms, fp32 weights: 68 us, with bf16 weights (kAny): 129;
+//     without w_post, bf16 weights (kAny): 100 us (403 MB each; 61 us)
 //
 // Parameter gradients are column sums over tokens: block b of a grid whose size is a function
 // of (T, H, type) adds rows b, b + blocks, ... into its registers and writes one partial row; a
@@ -142,11 +147,11 @@ __device__ __forceinline__ void drop2(const uint32_t (&w)[4], uint32_t threshold
     }
 }
 
-// What a call has: kAny looks as it goes; kAll and kAllDrop are the usual call, with both norms
-// (backward: dr and room for the ring too) and fp32 parameters, without and with dropout. In the
-// kernel of a block a row they also mean rows that fill their threads, elsewhere FULL says so.
-// Bound by instructions, the looking costs: a fifth of the backward's were branches and their
-// constants (16384 x 1000 bf16 90 us with it, 62 without).
+// What a call has: kAny looks as it goes; kAll and kAllDrop are calls with both norms (backward: dr
+// and room for the ring too) and fp32 parameters, without and with dropout. In the kernel of a block
+// a row they also mean rows that fill their threads, elsewhere FULL says so. Looking costs the
+// backward: a fifth of its instructions were branches and their constants (16384 x 1000 bf16 90 us
+// with it, 62 without). A block without w_post, or with weights of the rows' type, takes kAny.
 enum { kAny = 0, kAll = 1, kAllDrop = 2 };
 
 constexpr int kRowsAhead = 2;  // rows on their way in residual_norm_rows_kernel
@@ -465,8 +470,13 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT)
 // vectors of the next rows to a ring in shared memory (cp.async, no barrier) and reads them back,
 // twice, when their row comes. Consecutive lanes copy consecutive words: of fp32, where a vector is
 // two words, a lane copies one of its own and one of another's (8192 x 2048: 76 us, 112 with
-// every lane copying its own two). Rows too wide
-// for a stage of the ring (fp32 above H = 8192) are read from memory instead.
+// every lane copying its own two). The ring has as many stages, up to 4, as fit in shared memory;
+// rows of which not even one fits are read from memory (fp32 with r, dn, dr and y above H = 14336,
+// with a full gate besides above 11264).
+//
+// Above H = 8192 a block has more than 512 threads, 64 registers each, and the sums spill (496 to
+// 656 bytes of stores a thread): 4096 x 12288 bf16 261 us, 16384 341; 2048 x 12288 fp32 212, 16384
+// 360; against 92, 123, 92 and 123 us at the copy's rate.
 struct BwdRing {
     int32_t stages, arrays;               // stages 0: no ring
     int32_t i_r, i_dn, i_dr, i_y, i_gate; // place of each array in a stage, -1: absent
@@ -805,8 +815,10 @@ __global__ void __launch_bounds__(MAXT == 32 ? 128 : MAXT, MAXT == 32    ? 4
 
 // out[slot][column] = sum over the partial rows in order: a warp takes 32 columns of a slice of
 // the rows, the slices of a block are added in order. Bound by the latency of the loads, hence
-// all of a slice's rows (19 of the usual 296) at once and blocks that are all resident together:
-// 5 us for 296 x 3 x 4096, 7 us with 32 slices of 8 loads at a time.
+// 20 rows of a slice at once (all 19 of them at the 296 partials of 4096 columns; the 592 of
+// narrower rows take two rounds) and blocks that are all resident together: 6 us for 296 x 3 x 4096
+// right behind the backward, with the partials in L2 (9.2 from memory); two more with 32 slices of
+// 8 loads at a time.
 struct ReduceArgs {
     const float* part;
     int32_t parts, slots, H;
@@ -848,8 +860,9 @@ __global__ void __launch_bounds__(32 * kSlices) param_grad_kernel(ReduceArgs a)
 
 // out = keep ? x / probability : 0, each thread kVec vectors of 8, a block's width apart. A bf16
 // tensor moves 4 bytes an element and takes 15 instructions for it, 5 of them Philox's products
-// and xors: the integer pipes bound it (27.7 us for 16384 x 2048, 4.8 TB/s, 0.74 of the copy's
-// rate; 34 us with the keys formed per vector and a division per vector).
+// and xors (27.7 us for 16384 x 2048, 4.8 TB/s, 0.74 of the copy's rate; 34 us with the keys formed
+// per vector and a division per vector). No unit is full: the SM is at 0.53 of its throughput, with
+// 43 % of its warps resident; latency is left, of the loads or of Philox's dependent rounds.
 constexpr int kVec = 4;
 
 template <int DT>

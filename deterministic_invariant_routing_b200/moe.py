@@ -705,7 +705,9 @@ class MoEBlock:
     x is the residual stream, n its norm under this block's weight -- the n' that the block
     before returned, or residual_norm(x, w_next=...)[1] before the first one. w_post, gate ([H])
     and w_next are optional; p is the dropout probability of the training forward (a plain call
-    drops nothing). rng, first_row and row_ids: see dropout()."""
+    drops nothing). rng, first_row and row_ids: see dropout(). A training forward's ws belongs to
+    it until its backward: blocks, or steps, in flight at once need one each. So does a layer's own
+    workspace with calls or captured graphs that may run at the same time: a layer object each."""
 
     def __init__(self, layer: MoELayer, w_post=None, gate=None, w_next=None, eps: float = 1e-6,
                  residual_scale: float = 1.0, branch_scale: float = 1.0, p: float = 0.0):

@@ -425,7 +425,7 @@ typedef struct moe_norm_cfg {
  *   n = rms(r) * w_next
  * fp32 throughout, r and n rounded once to nearest even; n is taken from the rounded r, so
  * the call gives the bits of two calls, one for r and one for n. A row's result depends on
- * that row alone. Squares are summed in fp32: a row whose mean square overflows has rms 0.
+ * that row alone. Squares are summed in fp32: a row whose sum of squares overflows has rms 0.
  *
  *  x       [T,H].
  *  y       [T,H], the block's output, or NULL: then r is x, only n is computed, and w_post,
@@ -469,13 +469,13 @@ MOE_API int moe_residual_norm_backward(const moe_norm_cfg* cfg, const void* r, c
                                        size_t ws_bytes, void* stream);
 
 /*
- * Dropout whose mask is never stored: out = keep ? x / P(keep) : 0, rounded once. keep is a
- * function of (seed, offset, row, column): Philox4x32-10 with the key (seed low, seed high)
- * and the counter (column / 8, row, offset low, offset high) gives 16 bits for each of 8
- * columns (column 2 i of the eight in the low half of word i); an element is kept when they
- * are at least floor(65536 p + 1/2). P(keep) is that threshold's exact probability; p below
- * 2^-17 keeps everything. The backward is the same call on the gradient. Dropped infinities
- * and NaNs give 0.
+ * Dropout whose mask is never stored: out = keep ? x / P(keep) : 0, the fp32 product of x and
+ * fp32(1 / P(keep)), rounded to the type. keep is a function of (seed, offset, row, column):
+ * Philox4x32-10 with the key (seed low, seed high) and the counter (column / 8, row, offset low,
+ * offset high) gives 16 bits for each of 8 columns (column 2 i of the eight in the low half of
+ * word i); an element is kept when they are at least floor(65536 p + 1/2). P(keep) is that
+ * threshold's exact probability; p below 2^-17 keeps everything. The backward is the same call
+ * on the gradient. Dropped infinities and NaNs give 0.
  *
  *  T, H, dtype  as in moe_norm_cfg; x [T,H], out [T,H] (may be x).
  *  rng, first_row, row_ids as in moe_residual_norm.
